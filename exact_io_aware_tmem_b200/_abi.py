@@ -64,10 +64,44 @@ SIGNATURES = {
                                 c_void_p]),
     "fa_fwd_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                            c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_void_p]),
+    "fa_fwd_shaped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                              c_int, c_int, c_int, c_int, c_int, c_float, c_void_p, c_int, c_ll,
+                              c_void_p, c_void_p]),
+    "fa_bwd_shaped_workspace_size": (c_size_t, [c_ll, c_int, c_int, c_int, c_int]),
+    "fa_bwd_shaped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                              c_int, c_int, c_float, c_void_p, c_int, c_ll, c_void_p, c_void_p,
+                              c_size_t, c_void_p]),
+    "fa_key_ranges": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int,
+                              c_ll, c_void_p, c_void_p, c_void_p]),
+    "fa_decode_shaped_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int,
+                                                   c_int]),
+    "fa_decode_shaped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_ll,
+                                 c_int, c_int, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "fa_cache_evict_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "fa_cache_evict": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                               c_int, c_ll, c_int, c_void_p, c_void_p, c_ll, c_int, c_int,
+                               c_void_p, c_void_p, c_void_p, c_int, c_int, c_ll, c_void_p,
+                               c_void_p, c_void_p, c_ll, c_void_p, c_size_t, c_void_p]),
     "fa_version": (c_int, []),
     "fa_debug_build": (c_int, []),
     "fa_debug_set_trace": (c_int, [c_void_p, c_size_t, c_int]),
 }
+
+
+class ScoreShape(ctypes.Structure):
+    """fa_score_shape"""
+    _fields_ = [("softcap", c_float), ("alibi_slopes", c_void_p), ("key_begin", c_void_p),
+                ("key_end", c_void_p)]
+
+
+class DecodeShape(ctypes.Structure):
+    """fa_decode_shape"""
+    _fields_ = [("softcap", c_float), ("alibi_slopes", c_void_p), ("window", c_int),
+                ("key_positions", c_void_p), ("key_weights", c_void_p), ("slots", c_ll)]
+
+
 DEBUG_TRACE_BYTES = 32 * 1024 * 8
 DEBUG_LIB_PATH = os.path.join(PKG, "libfa_b200_debug.so")
 

@@ -13,6 +13,7 @@ Layouts (token-major, as in include/fa.h):
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import math
 from typing import Optional
 
@@ -70,11 +71,60 @@ def _shape(q: torch.Tensor, k: torch.Tensor, cu_seqlens, max_seqlen):
     return cu_seqlens.numel() - 1, 0, H, k.shape[1], D, int(max_seqlen), T
 
 
+@contextlib.contextmanager
+def _on(device: torch.device):
+    """The tensors' device as the current one: the library launches there."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        yield
+    else:
+        with torch.cuda.device(device):
+            yield
+
+
+def _aux(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
+         device: torch.device) -> Optional[int]:
+    """Pointer of an optional side tensor after its checks."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end):
+    """fa_score_shape of the arguments, or None when none is given."""
+    if softcap is None and alibi_slopes is None and key_begin is None and key_end is None:
+        return None
+    tokens = (q.shape[0],) if cu_seqlens is not None else tuple(q.shape[:2])
+    return _abi.ScoreShape(
+        0.0 if softcap is None else float(softcap),
+        _aux(alibi_slopes, "alibi_slopes", torch.float32, (q.shape[-2],), q.device),
+        _aux(key_begin, "key_begin", torch.int32, tokens, q.device),
+        _aux(key_end, "key_end", torch.int32, tokens, q.device))
+
+
+def _same(what: str, like: torch.Tensor, **tensors):
+    """Shape, type, layout and device of ``tensors`` are those of ``like``."""
+    for name, t in tensors.items():
+        if (t.shape != like.shape or t.dtype != like.dtype or not t.is_contiguous() or
+                t.device != like.device):
+            raise ValueError(f"{name} must match {what} in shape, dtype and device and be contiguous")
+
+
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
         scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
         max_seqlen: Optional[int] = None, out: Optional[torch.Tensor] = None,
-        lse: Optional[torch.Tensor] = None):
-    """Attention forward. Returns (O, LSE)."""
+        lse: Optional[torch.Tensor] = None, softcap: Optional[float] = None,
+        alibi_slopes: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+        key_end: Optional[torch.Tensor] = None):
+    """Attention forward. Returns (O, LSE).
+
+    Shaped scores (fa_fwd_shaped): ``softcap`` caps them by softcap *
+    tanh(x / softcap), ``alibi_slopes`` (float32 [H]) subtracts slope * |i - j|,
+    ``key_begin`` / ``key_end`` (int32 [B, N], packed [T]) limit each query to
+    keys [begin, end) of its sequence; ``key_ranges`` makes them. All elements
+    of q, k and v must then be finite.
+    """
     B, N, H, H_kv, D, max_sl, T = _shape(q, k, cu_seqlens, max_seqlen)
     if v.shape != k.shape or v.dtype != q.dtype or k.dtype != q.dtype:
         raise ValueError("k and v must match in shape and dtype with q's dtype")
@@ -84,6 +134,21 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = Fal
         lse = torch.empty((B, H, N) if cu_seqlens is None else (H, T), device=q.device,
                           dtype=torch.float32)
     s = -1.0 if scale is None else float(scale)
+    shape = _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end)
+    if shape is not None:
+        _same("k", k, v=v)
+        _same("q", q, out=out)
+        _aux(lse, "lse", torch.float32, (B, H, N) if cu_seqlens is None else (H, T), q.device)
+        if k.device != q.device or q.dtype != k.dtype or k.shape[-1] != D or k.dim() != q.dim() or \
+                k.shape[:-2] != q.shape[:-2]:
+            raise ValueError("k must match q but for its heads")
+        with _on(q.device):
+            st = _lib().fa_fwd_shaped(
+                _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, H_kv, N, D,
+                _DTYPES[q.dtype], int(bool(causal)), s, _ptr(cu_seqlens), max_sl, T,
+                ctypes.byref(shape), _stream(q.device))
+        _abi.check(st, "fa_fwd_shaped")
+        return out, lse
     st = _lib().fa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, H_kv, N, D,
                            _DTYPES[q.dtype], int(bool(causal)), s, _ptr(cu_seqlens), max_sl, T,
                            _stream(q.device))
@@ -105,8 +170,14 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
         max_seqlen: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
-        dv: Optional[torch.Tensor] = None, phases: int = BWD_FUSED):
+        dv: Optional[torch.Tensor] = None, phases: int = BWD_FUSED,
+        softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None,
+        key_begin: Optional[torch.Tensor] = None, key_end: Optional[torch.Tensor] = None):
     """Attention backward for the loss sum(O * dO). Returns (dQ, dK, dV).
+
+    ``softcap``, ``alibi_slopes``, ``key_begin`` and ``key_end`` as in the
+    ``fwd`` call that gave ``o`` and ``lse`` (fa_bwd_shaped; ``phases`` must
+    then be ``BWD_FUSED``, and the slopes get no gradient).
 
     ``phases`` selects the kernels to enqueue (the FA_BWD_PHASE_* bits of
     include/fa.h): the default ``BWD_FUSED`` runs the preprocess, the fused
@@ -121,6 +192,28 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
+    shape = _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end)
+    if shape is not None:
+        if phases != BWD_FUSED:
+            raise ValueError("shaped scores have the BWD_FUSED backward only")
+        _same("q", q, dout=dout, o=o, dq=dq)
+        _same("k", k, v=v, dk=dk, dv=dv)
+        _aux(lse, "lse", torch.float32, (B, H, N) if cu_seqlens is None else (H, T), q.device)
+        if k.device != q.device or q.dtype != k.dtype or k.shape[-1] != D or k.dim() != q.dim() or \
+                k.shape[:-2] != q.shape[:-2]:
+            raise ValueError("k must match q but for its heads")
+        need = int(_lib().fa_bwd_shaped_workspace_size(T, B, H, D, _DTYPES[q.dtype]))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(q.device):
+            st = _lib().fa_bwd_shaped(
+                _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+                _ptr(dv), B, H, H_kv, N, D, _DTYPES[q.dtype], int(bool(causal)),
+                -1.0 if scale is None else float(scale), _ptr(cu_seqlens), max_sl, T,
+                ctypes.byref(shape), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                _stream(q.device))
+        _abi.check(st, "fa_bwd_shaped")
+        return dq, dk, dv
     need = workspace_size(T, H, D, q.dtype, phases)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -133,6 +226,50 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                   _stream(q.device))
     _abi.check(st, "fa_bwd")
     return dq, dk, dv
+
+
+def key_ranges(N: Optional[int] = None, *, B: int = 1, causal: bool = True,
+               doc_ids: Optional[torch.Tensor] = None,
+               prefix_lens: Optional[torch.Tensor] = None, window: Optional[int] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: Optional[int] = None,
+               device="cuda"):
+    """Key ranges (begin, end) of every query token for ``fwd`` and ``bwd`` (fa_key_ranges).
+
+    ``doc_ids`` (int32, one per token): queries see their own document, the run
+    of equal ids around them. ``prefix_lens`` (int32 [B], with ``causal``): the
+    first keys that every query of the sequence sees. ``window``: the last keys,
+    the token itself counted. Dense: [B, N]; packed (``cu_seqlens``): [N], N the
+    total number of tokens. The ranges hold the causal limit; pass
+    ``causal=False`` with them to ``fwd`` when there are prefixes.
+    """
+    if N is None:
+        if doc_ids is None:
+            raise ValueError("key_ranges needs N or doc_ids")
+        N = int(doc_ids.shape[-1])
+        B = int(doc_ids.shape[0]) if doc_ids.dim() == 2 and cu_seqlens is None else B
+    for t in (cu_seqlens, doc_ids, prefix_lens):
+        if t is not None:
+            device = t.device
+            break
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    if cu_seqlens is not None:
+        if max_seqlen is None:
+            raise ValueError("packed inputs need max_seqlen")
+        B = cu_seqlens.numel() - 1
+        _aux(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), device)
+    tokens = (N,) if cu_seqlens is not None else (B, N)
+    docs = _aux(doc_ids, "doc_ids", torch.int32, tokens, device)
+    prefix = _aux(prefix_lens, "prefix_lens", torch.int32, (B,), device)
+    begin, end = (torch.empty(tokens, dtype=torch.int32, device=device) for _ in range(2))
+    with _on(device):
+        st = _lib().fa_key_ranges(docs, prefix, 0 if window is None else int(window),
+                                  int(bool(causal)), B, 0 if cu_seqlens is not None else N,
+                                  _ptr(cu_seqlens), int(max_seqlen or 0), N, _ptr(begin),
+                                  _ptr(end), _stream(device))
+    _abi.check(st, "fa_key_ranges")
+    return begin, end
 
 
 def decode_num_splits(B: int, H_kv: int, max_seqlen_k: int, n_split: int = 0) -> int:
@@ -156,12 +293,22 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
            block_table: Optional[torch.Tensor] = None, page_size: Optional[int] = None,
            causal: bool = True, scale: Optional[float] = None, n_split: int = 0,
            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-           workspace: Optional[torch.Tensor] = None):
+           workspace: Optional[torch.Tensor] = None, softcap: Optional[float] = None,
+           alibi_slopes: Optional[torch.Tensor] = None, window: Optional[int] = None,
+           key_positions: Optional[torch.Tensor] = None,
+           key_weights: Optional[torch.Tensor] = None):
     """Split-KV decode (fa_decode): O [B*q_len, H, D] bf16 and LSE [B*q_len, H].
 
     ``q`` is [B*q_len, H, D]; the caches are [rows, H_kv, D]. Contiguous
     cache: ``page_size`` is the rows per sequence (default: rows // B).
     Paged cache: ``block_table`` [B, max_blocks] int32 and ``page_size``.
+
+    Shaped scores (fa_decode_shaped; automatic splits, at most 64 query rows per
+    kv head): ``softcap`` and ``alibi_slopes`` as in ``fwd``, ``window`` the last
+    positions a query sees, ``key_positions`` (int32 [B, H_kv, slots]) the
+    positions of a cache that has lost slots. ``key_weights`` (float32 [B, H_kv,
+    slots]) is increased in place by the attention weight each slot receives;
+    ``evict`` reads it.
     """
     B = cache_seqlens.numel()
     H, D = q.shape[1], q.shape[2]
@@ -174,6 +321,11 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((q.shape[0], H), device=q.device, dtype=torch.float32)
+    if not (softcap is None and alibi_slopes is None and window is None and
+            key_positions is None and key_weights is None):
+        return _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, block_table,
+                              page_size, causal, scale, n_split, out, lse, workspace, softcap,
+                              alibi_slopes, window, key_positions, key_weights)
     need = decode_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k, n_split)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
@@ -184,6 +336,119 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _ptr(workspace) if need else None, need, _stream(q.device))
     _abi.check(st, "fa_decode")
     return out, lse
+
+
+def _check_cache(k_cache, v_cache, cache_seqlens, block_table):
+    """Device, type and layout of a cache as decode and evict take it."""
+    dev = k_cache.device
+    if k_cache.dim() != 3 or k_cache.dtype != torch.bfloat16 or not k_cache.is_cuda or \
+            not k_cache.is_contiguous():
+        raise ValueError("a cache is a contiguous bfloat16 CUDA tensor [rows, H_kv, D]")
+    _same("k_cache", k_cache, v_cache=v_cache)
+    _aux(cache_seqlens, "cache_seqlens", torch.int32, tuple(cache_seqlens.shape), dev)
+    if block_table is not None:
+        _aux(block_table, "block_table", torch.int32,
+             (cache_seqlens.numel(), block_table.shape[-1]), dev)
+
+
+def _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, block_table, page_size,
+                   causal, scale, n_split, out, lse, workspace, softcap, alibi_slopes, window,
+                   key_positions, key_weights):
+    if n_split != 0:
+        raise ValueError("shaped scores take automatic splits only (n_split = 0)")
+    B, (_, H, D) = cache_seqlens.numel(), q.shape
+    rows, H_kv = k_cache.shape[:2]
+    dev = q.device
+    _check_cache(k_cache, v_cache, cache_seqlens, block_table)
+    if k_cache.device != dev or k_cache.shape[2] != D or q.dtype != torch.bfloat16 or \
+            not q.is_contiguous() or q.shape[0] != B * q_len:
+        raise ValueError("q must be a contiguous bfloat16 tensor [B * q_len, H, D] beside the cache")
+    _same("q", q, out=out)
+    _aux(lse, "lse", torch.float32, (q.shape[0], H), dev)
+    slots = next((t.shape[-1] for t in (key_weights, key_positions) if t is not None), 0)
+    shape = _abi.DecodeShape(
+        0.0 if softcap is None else float(softcap),
+        _aux(alibi_slopes, "alibi_slopes", torch.float32, (H,), dev),
+        0 if window is None else int(window),
+        _aux(key_positions, "key_positions", torch.int32, (B, H_kv, slots), dev),
+        _aux(key_weights, "key_weights", torch.float32, (B, H_kv, slots), dev), slots)
+    with _on(dev):
+        need = int(_lib().fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k,
+                                                          int(key_weights is not None)))
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        st = _lib().fa_decode_shaped(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cache_seqlens),
+            _ptr(block_table), B, int(q_len), H, H_kv, D, int(page_size),
+            0 if block_table is None else block_table.shape[1], rows, int(max_seqlen_k),
+            int(bool(causal)), -1.0 if scale is None else float(scale), ctypes.byref(shape),
+            _ptr(workspace) if need else None, need, _stream(dev))
+    _abi.check(st, "fa_decode_shaped")
+    return out, lse
+
+
+def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_seqlens: torch.Tensor,
+          key_weights: torch.Tensor, *, keep: int, max_seqlen_k: int, recent: int = 0,
+          block_table: Optional[torch.Tensor] = None, page_size: Optional[int] = None,
+          key_positions: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+          v_out: Optional[torch.Tensor] = None, out_block_table: Optional[torch.Tensor] = None,
+          out_page_size: Optional[int] = None, out_slots: Optional[int] = None,
+          workspace: Optional[torch.Tensor] = None):
+    """Copy the slots worth keeping of a cache into another one (fa_cache_evict).
+
+    Each (sequence, kv head) keeps its last ``recent`` slots and the others with
+    the largest ``key_weights`` (float32 [B, H_kv, slots], as ``decode`` adds
+    them up), ``keep`` in all, in their order. Returns (k_out, v_out,
+    seqlens int32 [B], weights float32 and positions int32 [B, H_kv,
+    out_slots]); weights are 0 and positions -1 from the new length on, ready
+    for new tokens. ``key_positions`` are those of a cache that has lost slots
+    before. The caches are laid out as for ``decode``; without ``k_out`` and
+    ``v_out`` a contiguous pair of ``out_page_size`` (default ``out_slots``)
+    rows a sequence is allocated, zeroed. ``out_slots`` defaults to ``keep``.
+    """
+    _check_cache(k_cache, v_cache, cache_seqlens, block_table)
+    dev = k_cache.device
+    B, (rows, H_kv, D) = cache_seqlens.numel(), k_cache.shape
+    if block_table is None and page_size is None:
+        page_size = rows // max(B, 1)
+    if block_table is not None and page_size is None:
+        raise ValueError("a paged cache needs page_size")
+    out_slots = int(keep) if out_slots is None else int(out_slots)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        if out_block_table is not None:
+            raise ValueError("out_block_table needs k_out and v_out")
+        out_page_size = out_slots if out_page_size is None else int(out_page_size)
+        k_out, v_out = (torch.zeros((B * out_page_size, H_kv, D), dtype=k_cache.dtype, device=dev)
+                        for _ in range(2))
+    elif out_page_size is None:
+        if out_block_table is not None:
+            raise ValueError("a paged cache needs out_page_size")
+        out_page_size = k_out.shape[0] // max(B, 1)
+    _check_cache(k_out, v_out, cache_seqlens, out_block_table)
+    if k_out.device != dev or k_out.shape[1:] != k_cache.shape[1:]:
+        raise ValueError("k_out must have the cache's heads, head size and device")
+    slots = key_weights.shape[-1]
+    w = _aux(key_weights, "key_weights", torch.float32, (B, H_kv, slots), dev)
+    pos = _aux(key_positions, "key_positions", torch.int32, (B, H_kv, slots), dev)
+    seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
+    weights = torch.empty((B, H_kv, out_slots), dtype=torch.float32, device=dev)
+    positions = torch.empty((B, H_kv, out_slots), dtype=torch.int32, device=dev)
+    need = int(_lib().fa_cache_evict_workspace_size(B, H_kv, int(keep)))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    with _on(dev):
+        st = _lib().fa_cache_evict(
+            _ptr(k_cache), _ptr(v_cache), _ptr(cache_seqlens), _ptr(block_table), B, H_kv, D,
+            int(page_size), 0 if block_table is None else block_table.shape[1], rows,
+            int(max_seqlen_k), w, pos, slots, int(keep), int(recent), _ptr(k_out), _ptr(v_out),
+            _ptr(out_block_table), int(out_page_size),
+            0 if out_block_table is None else out_block_table.shape[1], k_out.shape[0],
+            _ptr(seqlens), _ptr(weights), _ptr(positions), out_slots, _ptr(workspace), need,
+            _stream(dev))
+    _abi.check(st, "fa_cache_evict")
+    return k_out, v_out, seqlens, weights, positions
 
 
 def fp8_quantize(x: torch.Tensor, B: int, N: int, *, out: Optional[torch.Tensor] = None,
@@ -219,7 +484,6 @@ def fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor, q_scale: torch.
 
 def check_device_error(device: Optional[torch.device] = None) -> tuple:
     """Synchronise the current stream; return (status, where) and clear the flag."""
-    import ctypes
     dev = torch.device("cuda") if device is None else device
     where = ctypes.c_uint(0)
     st = _lib().fa_check_device_error(_stream(dev), ctypes.byref(where))

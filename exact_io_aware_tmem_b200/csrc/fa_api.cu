@@ -11,6 +11,7 @@
 #include "decode_t.h"
 #include "fwd_d64.h"
 #include "ex2_fma.cuh"
+#include "host.h"
 #include "params.h"
 
 namespace fa {
@@ -41,6 +42,8 @@ constexpr int kMaxDevices = 64;
 unsigned* g_err_ptr[kMaxDevices] = {};
 std::mutex g_mu;
 
+}  // namespace
+
 // Device address of g_err_word on the current device (looked up once).
 unsigned* err_word() {
   int dev = 0;
@@ -53,6 +56,8 @@ unsigned* err_word() {
   }
   return g_err_ptr[dev];
 }
+
+namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -72,6 +77,8 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+}  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -118,7 +125,77 @@ fa_status check_common(AttnParams& p, int B, int H, int H_kv, int N, int D, fa_d
   return FA_OK;
 }
 
-}  // namespace
+fa_status check_cache(int B, const int* block_table, int page_size, int max_blocks,
+                      long long cache_rows, int max_seqlen_k) {
+  if (page_size <= 0 || cache_rows < 1) return FA_ERR_INVALID_ARG;
+  if (block_table == nullptr) {
+    if (page_size < max_seqlen_k) return FA_ERR_INVALID_ARG;
+    if (cache_rows < static_cast<long long>(B - 1) * page_size + max_seqlen_k)
+      return FA_ERR_INVALID_ARG;
+  } else {
+    if (page_size % 16 != 0 || !(128 % page_size == 0 || page_size % 128 == 0))
+      return FA_ERR_UNSUPPORTED;
+    if (max_blocks < (max_seqlen_k + page_size - 1) / page_size || cache_rows % page_size != 0)
+      return FA_ERR_INVALID_ARG;
+  }
+  return FA_OK;
+}
+
+fa_status check_decode(AttnParams& p, DecodeArgs& d, bool& empty, const void* q,
+                       const void* k_cache, const void* v_cache, void* o, float* lse,
+                       const int* cache_seqlens, const int* block_table, int B, int q_len, int H,
+                       int H_kv, int D, int page_size, int max_blocks, long long cache_rows,
+                       int max_seqlen_k, int causal, float scale) {
+  empty = false;
+  if (B < 0 || q_len <= 0 || H <= 0 || H_kv <= 0 || D <= 0 || max_seqlen_k < 0 || cache_rows < 0)
+    return FA_ERR_INVALID_ARG;
+  if (H % H_kv != 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  const int g = H / H_kv;
+  if (static_cast<long long>(q_len) * g > 128) return FA_ERR_UNSUPPORTED;
+  if (cache_rows >= (1ll << 31) || static_cast<long long>(B) * q_len > INT32_MAX ||
+      static_cast<long long>(B) * H_kv > (1ll << 24))
+    return FA_ERR_UNSUPPORTED;
+  if (B == 0) {
+    empty = true;
+    return FA_OK;
+  }
+  const fa_status st = check_cache(B, block_table, page_size, max_blocks, cache_rows, max_seqlen_k);
+  if (st != FA_OK) return st;
+  if (!q || !k_cache || !v_cache || !o || !lse || !cache_seqlens) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o))
+    return FA_ERR_INVALID_ARG;
+  p = {};
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.o = o;
+  p.lse = lse;
+  p.B = B;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.D = D;
+  p.N = 0;
+  p.causal = causal;
+  p.max_seqlen = max_seqlen_k;
+  p.total = static_cast<long long>(B) * q_len;
+  if (!(scale > 0.f) || !isfinite(scale)) scale = 1.f / sqrtf(static_cast<float>(D));
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err.budget = g_budget;
+  p.trace = g_trace;
+  p.trace_cta = g_trace_cta;
+  d = {};
+  d.cache_seqlens = cache_seqlens;
+  d.block_table = block_table;
+  d.page = page_size;
+  d.max_blocks = (block_table != nullptr) ? max_blocks : 0;
+  d.cache_rows = cache_rows;
+  d.q_len = q_len;
+  d.g = g;
+  d.n_rows = q_len * g;
+  return FA_OK;
+}
 
 fa_status record_cuda(cudaError_t e) { return cuda_status(e); }
 
@@ -290,69 +367,21 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     int H_kv, int D, int page_size, int max_blocks, long long cache_rows,
                     int max_seqlen_k, int causal, float scale, int n_split, void* workspace,
                     size_t ws_bytes, fa_stream_t stream) {
-  if (B < 0 || q_len <= 0 || H <= 0 || H_kv <= 0 || D <= 0 || max_seqlen_k < 0 ||
-      cache_rows < 0 || n_split < 0)
-    return FA_ERR_INVALID_ARG;
-  if (H % H_kv != 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  const int g = H / H_kv;
-  if (static_cast<long long>(q_len) * g > 128) return FA_ERR_UNSUPPORTED;
-  if (cache_rows >= (1ll << 31) || static_cast<long long>(B) * q_len > INT32_MAX ||
-      static_cast<long long>(B) * H_kv > (1ll << 24))
-    return FA_ERR_UNSUPPORTED;
-  if (B == 0) return FA_OK;
-  if (page_size <= 0 || cache_rows < 1) return FA_ERR_INVALID_ARG;
-  if (block_table == nullptr) {
-    if (page_size < max_seqlen_k) return FA_ERR_INVALID_ARG;
-    if (cache_rows < static_cast<long long>(B - 1) * page_size + max_seqlen_k)
-      return FA_ERR_INVALID_ARG;
-  } else {
-    if (page_size % 16 != 0 || !(128 % page_size == 0 || page_size % 128 == 0))
-      return FA_ERR_UNSUPPORTED;
-    if (max_blocks < (max_seqlen_k + page_size - 1) / page_size || cache_rows % page_size != 0)
-      return FA_ERR_INVALID_ARG;
-  }
-  if (!q || !k_cache || !v_cache || !o || !lse || !cache_seqlens) return FA_ERR_INVALID_ARG;
-  if (!fa::aligned16(q) || !fa::aligned16(k_cache) || !fa::aligned16(v_cache) ||
-      !fa::aligned16(o))
-    return FA_ERR_INVALID_ARG;
+  if (n_split < 0) return FA_ERR_INVALID_ARG;
+  AttnParams p = {};
+  fa::DecodeArgs d = {};
+  bool empty = false;
+  const fa_status st = fa::check_decode(p, d, empty, q, k_cache, v_cache, o, lse, cache_seqlens,
+                                        block_table, B, q_len, H, H_kv, D, page_size, max_blocks,
+                                        cache_rows, max_seqlen_k, causal, scale);
+  if (st != FA_OK || empty) return st;
   const int ns = fa_decode_num_splits(B, H_kv, max_seqlen_k, n_split);
   const size_t need = fa_decode_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k, n_split);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || !fa::aligned16(workspace)))
     return FA_ERR_INVALID_ARG;
 
-  AttnParams p = {};
-  p.q = q;
-  p.k = k_cache;
-  p.v = v_cache;
-  p.o = o;
-  p.lse = lse;
-  p.B = B;
-  p.H = H;
-  p.H_kv = H_kv;
-  p.D = D;
-  p.N = 0;
-  p.causal = causal;
-  p.max_seqlen = max_seqlen_k;
-  p.total = static_cast<long long>(B) * q_len;
-  if (!(scale > 0.f) || !isfinite(scale)) scale = 1.f / sqrtf(static_cast<float>(D));
-  p.scale = scale;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.err.budget = fa::g_budget;
   p.err.word = fa::err_word();
   if (p.err.word == nullptr) return FA_ERR_CUDA;
-  p.trace = fa::g_trace;
-  p.trace_cta = fa::g_trace_cta;
-
-  fa::DecodeArgs d = {};
-  d.cache_seqlens = cache_seqlens;
-  d.block_table = block_table;
-  d.page = page_size;
-  d.max_blocks = (block_table != nullptr) ? max_blocks : 0;
-  d.cache_rows = cache_rows;
-  d.q_len = q_len;
-  d.g = g;
-  d.n_rows = q_len * g;
   d.n_split = ns;
   const int tiles = std::max(1, (max_seqlen_k + 127) / 128);
   d.chunk = (tiles + ns - 1) / ns;

@@ -1,0 +1,107 @@
+// Attention with shaped scores: what the kernels of fa_fwd_shaped,
+// fa_bwd_shaped, fa_decode_shaped and fa_cache_evict share.
+//
+// The scores of include/fa.h, "Shaped scores":
+//     z_ij = cap tanh(scale q_i.k_j / cap) - slope_h |i - j|,
+// key j visible to query i iff begin_i <= j < end_i (and j <= i when causal).
+#pragma once
+
+#include "params.h"
+
+namespace fa {
+
+struct ShapeArgs {
+  float cap;               // 0: no cap
+  float scale_over_cap;    // scale / cap (cap > 0)
+  const float* slopes;     // [H] or null
+  const int* key_begin;    // [T] or null
+  const int* key_end;      // [T] or null
+};
+
+// Visible keys [lo, hi) of the query at position i of a sequence; an empty
+// range is returned as [0, 0). Ranges reaching outside the sequence are
+// clipped to it.
+struct KeyRange {
+  int lo, hi;
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnParams& p, const ShapeArgs& sh,
+                                              const SeqInfo& s, int i) {
+  int lo = 0, hi = s.len;
+  if (sh.key_begin != nullptr) lo = max(0, __ldg(sh.key_begin + s.start + i));
+  if (sh.key_end != nullptr) hi = min(hi, __ldg(sh.key_end + s.start + i));
+  if (p.causal) hi = min(hi, i + 1);
+  if (lo >= hi) lo = hi = 0;
+  return {lo, hi};
+}
+
+// Decode over a cache: what fa_decode_shape adds to a decode's arguments.
+struct DecodeShapeArgs {
+  float cap;
+  float scale_over_cap;
+  const float* slopes;         // [H] or null
+  int window;                  // 0: none
+  const int* key_positions;    // [B, H_kv, slots] or null: the slot is the position
+  float* key_weights;          // [B, H_kv, slots] or null
+  long long slots;
+};
+
+// Eviction: keep the last ``recent`` slots and the heaviest others.
+struct EvictArgs {
+  const void* k;
+  const void* v;
+  const int* cache_seqlens;
+  const int* block_table;      // null: contiguous
+  int B, H_kv, D;
+  int page, max_blocks;
+  long long cache_rows;
+  int max_len;
+  const float* key_weights;    // [B, H_kv, slots]
+  const int* key_positions;    // [B, H_kv, slots] or null
+  long long slots;
+  int keep, recent;
+  void* k_out;
+  void* v_out;
+  const int* out_table;        // null: contiguous
+  int out_page, out_max_blocks;
+  long long out_rows;
+  int* seqlens_out;            // [B]
+  float* weights_out;          // [B, H_kv, out_slots]
+  int* positions_out;          // [B, H_kv, out_slots]
+  long long out_slots;
+  int* src;                    // workspace: [B, H_kv, keep] slots kept, ascending
+  DevErr err;
+};
+
+// Cache row of slot j of sequence b (include/fa.h, fa_decode), or -1 for a
+// block-table entry outside the cache.
+__device__ __forceinline__ long long cache_row(const int* table, int max_blocks, int page,
+                                               long long rows, int b, int j) {
+  long long r;
+  if (table == nullptr) {
+    r = static_cast<long long>(b) * page + j;
+  } else {
+    const int pg = j / page;
+    if (pg >= max_blocks) return -1;
+    r = static_cast<long long>(__ldg(table + static_cast<size_t>(b) * max_blocks + pg)) * page +
+        j % page;
+  }
+  return (r >= 0 && r < rows) ? r : -1;
+}
+
+__device__ __forceinline__ void record_bounds(const DevErr& e, unsigned where) {
+  atomicOr(e.word, ERR_BOUNDS);
+  atomicExch(e.word + 1, where);
+}
+
+cudaError_t launch_shaped_fwd_simt(const AttnParams& p, const ShapeArgs& sh, bool f32,
+                                   cudaStream_t stream);
+cudaError_t launch_shaped_bwd_simt(const AttnParams& p, const ShapeArgs& sh, bool f32,
+                                   cudaStream_t stream);
+cudaError_t launch_key_ranges(const AttnParams& p, const int* doc_ids, const int* prefix_lens,
+                              int window, int* key_begin, int* key_end, cudaStream_t stream);
+cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,
+                                 const DecodeShapeArgs& sh, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
+}  // namespace fa

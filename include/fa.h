@@ -410,6 +410,168 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v, const float*
                      const float* k_scale, void* o, float* lse, int B, int H, int H_kv, int N,
                      int D, int causal, float scale, fa_stream_t stream);
 
+/*
+ * --------------------------------------------------------- shaped scores ---
+ * Attention whose scores are capped, biased by distance, or limited to a range
+ * of keys per query:
+ *     x_ij = scale q_i . k_j
+ *     z_ij = softcap * tanh(x_ij / softcap) - alibi_slopes[h] * |i - j|
+ *     key j is visible to query i iff key_begin[i] <= j < key_end[i]
+ *                                 (and j <= i when causal)
+ *     O_i = sum_j softmax_j(z_ij) v_j over the visible keys, LSE_i likewise.
+ * A query that sees no key gets O = 0, LSE = -inf and a zero gradient, and adds
+ * nothing to dK and dV. The ranges express document masks, prefix masks and
+ * windows (fa_key_ranges makes them); tiles that no query sees are skipped.
+ * The pages ask for masks and padding without answering ("Flash Attention
+ * self-test", section C); the cap, the bias and the ranges are this library's.
+ *
+ *   softcap       > 0 and finite; 0: no cap
+ *   alibi_slopes  device float32 [H], or NULL: no bias. Constants: they get no
+ *                 gradient.
+ *   key_begin,    device int32, one entry per token ([B, N] dense, [T] packed),
+ *   key_end       counted from the start of the token's own sequence, or NULL
+ *                 (0 / the sequence's length). Entries outside the sequence
+ *                 are clipped to it; begin >= end means no key.
+ * Every element of q, k, v and dout must be finite, of tokens that no query
+ * sees too: a masked probability is 0 and multiplies what lies there.
+ * A NULL shape, or one with nothing set, is fa_fwd / fa_bwd.
+ */
+typedef struct {
+  float softcap;
+  const float* alibi_slopes;
+  const int* key_begin;
+  const int* key_end;
+} fa_score_shape;
+
+/* fa_fwd_shaped - fa_fwd with shaped scores; arguments, types, layouts and
+ * errors as for fa_fwd. */
+fa_status fa_fwd_shaped(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                        int H, int H_kv, int N, int D, fa_dtype dtype, int causal, float scale,
+                        const int* cu_seqlens, int max_seqlen, long long total_tokens,
+                        const fa_score_shape* shape, fa_stream_t stream);
+
+/* fa_bwd_shaped_workspace_size - bytes of device scratch of fa_bwd_shaped for
+ * B sequences with ``total_tokens`` tokens in all. Returns 0 for invalid
+ * sizes. */
+size_t fa_bwd_shaped_workspace_size(long long total_tokens, int B, int H, int D, fa_dtype dtype);
+
+/*
+ * fa_bwd_shaped - gradients of fa_fwd_shaped for the loss sum(O * dO):
+ *   P = exp(z - LSE), dV = P^T dO, dZ = P * (dO V^T - D_i), D_i = dO_i . O_i,
+ *   dX = dZ * (1 - tanh(x / softcap)^2), dQ = scale dX K, dK = scale dX^T Q.
+ * Arguments as for fa_bwd and the fa_fwd_shaped call that gave o and lse. For
+ * bf16 dQ is reproducible to rounding only (its fp32 additions over key tiles
+ * have no fixed order); dK and dV are bitwise reproducible.
+ */
+fa_status fa_bwd_shaped(const void* q, const void* k, const void* v, const void* o,
+                        const float* lse, const void* dout, void* dq, void* dk, void* dv, int B,
+                        int H, int H_kv, int N, int D, fa_dtype dtype, int causal, float scale,
+                        const int* cu_seqlens, int max_seqlen, long long total_tokens,
+                        const fa_score_shape* shape, void* workspace, size_t ws_bytes,
+                        fa_stream_t stream);
+
+/*
+ * fa_key_ranges - key_begin / key_end of every token from document ids, prefix
+ * lengths and a window:
+ *   the token's document is the run of equal neighbouring doc_ids around it
+ *   (doc_ids NULL: its whole sequence), [ds, de);
+ *   begin = ds, with a window > 0 at least i - window + 1;
+ *   end = de, with causal at most max(i + 1, prefix_lens[sequence]).
+ * The ranges hold the causal limit: pass causal = 0 with them when there are
+ * prefixes.
+ *   doc_ids      device int32 [T] or NULL
+ *   prefix_lens  device int32 [B] or NULL; needs causal = 1
+ *   window       0: none; a window counts the token itself
+ *   key_begin, key_end  out, device int32 [T]
+ */
+fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, int causal, int B,
+                        int N, const int* cu_seqlens, int max_seqlen, long long total_tokens,
+                        int* key_begin, int* key_end, fa_stream_t stream);
+
+/*
+ * fa_decode_shaped - fa_decode with shaped scores, and with the attention
+ * weights of the keys added up for fa_cache_evict. Query token i of q_len sits
+ * in slot cache_seqlens[b] - q_len + i. A slot's position is its number, or
+ * key_positions' entry where a cache has lost slots; distances and the window
+ * are between positions:
+ *     z = softcap * tanh(x / softcap) - alibi_slopes[h] * |pos_i - pos_j|
+ *     visible: slot j <= slot i (causal) and pos_i - pos_j < window
+ *   softcap, alibi_slopes  as above
+ *   window         0: none
+ *   key_positions  device int32 [B, H_kv, slots], >= 0 and ascending over a
+ *                  sequence's slots, or NULL. (A query token before slot 0 has
+ *                  its negative slot number for a position.)
+ *   key_weights    device float32 [B, H_kv, slots] or NULL. Entry (b, hk, j),
+ *                  j < cache_seqlens[b], is increased by the sum of the softmax
+ *                  weights that the q_len tokens x H / H_kv heads of key/value
+ *                  head hk give to slot j; the other entries stay as they are.
+ *   slots          row length of the two, >= max_seqlen_k
+ * The rest as for fa_decode with n_split = 0, but at most 64 query rows share
+ * a key/value head (q_len * H / H_kv <= 64, else FA_ERR_UNSUPPORTED). Results
+ * are bitwise reproducible.
+ */
+typedef struct {
+  float softcap;
+  const float* alibi_slopes;
+  int window;
+  const int* key_positions;
+  float* key_weights;
+  long long slots;
+} fa_decode_shape;
+
+/* fa_decode_shaped_workspace_size - bytes of workspace of fa_decode_shaped;
+ * ``weights``: whether key_weights is set. Host only; 0 for invalid sizes. */
+size_t fa_decode_shaped_workspace_size(int B, int q_len, int H, int H_kv, int D, int max_seqlen_k,
+                                       int weights);
+
+fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cache, void* o,
+                           float* lse, const int* cache_seqlens, const int* block_table, int B,
+                           int q_len, int H, int H_kv, int D, int page_size, int max_blocks,
+                           long long cache_rows, int max_seqlen_k, int causal, float scale,
+                           const fa_decode_shape* shape, void* workspace, size_t ws_bytes,
+                           fa_stream_t stream);
+
+/*
+ * fa_cache_evict - copies the slots worth keeping of a bf16 cache into another
+ * one. Each (sequence b, kv head) keeps n = min(cache_seqlens[b], keep) slots:
+ * the last min(recent, n), and of the others those with the largest
+ * key_weights (equal weights: the lower slot; NaN counts as the least). They
+ * keep their order. Heads keep different slots, so a row of the new cache holds
+ * the heads of different tokens; positions_out says which.
+ *   k_cache .. max_seqlen_k  as for fa_decode; D a multiple of 8, at most 256
+ *   key_weights    device float32 [B, H_kv, slots]
+ *   key_positions  device int32 [B, H_kv, slots] or NULL (the slot's number)
+ *   slots          >= max_seqlen_k
+ *   keep, recent   0 < keep, 0 <= recent <= keep
+ *   k_out, v_out, out_block_table, out_page_size, out_max_blocks, out_rows
+ *                  the new cache, laid out as for fa_decode. Rows past a
+ *                  sequence's n slots are left as they are. The two caches may
+ *                  overlap only where both are paged, in pages that this call
+ *                  does not read.
+ *   seqlens_out    out, device int32 [B]: n
+ *   weights_out    out, device float32 [B, H_kv, out_slots]: the kept weights,
+ *                  0 from n on
+ *   positions_out  out, device int32 [B, H_kv, out_slots]: the kept positions,
+ *                  -1 from n on
+ *   out_slots      >= min(keep, max_seqlen_k)
+ *   workspace      device, 16-byte aligned, at least
+ *                  fa_cache_evict_workspace_size(B, H_kv, keep) bytes
+ * The outputs must not overlap the inputs. A cache_seqlens entry outside
+ * [0, max_seqlen_k] is reported by fa_check_device_error, and that sequence is
+ * left unwritten.
+ */
+size_t fa_cache_evict_workspace_size(int B, int H_kv, int keep);
+
+fa_status fa_cache_evict(const void* k_cache, const void* v_cache, const int* cache_seqlens,
+                         const int* block_table, int B, int H_kv, int D, int page_size,
+                         int max_blocks, long long cache_rows, int max_seqlen_k,
+                         const float* key_weights, const int* key_positions, long long slots,
+                         int keep, int recent, void* k_out, void* v_out,
+                         const int* out_block_table, int out_page_size, int out_max_blocks,
+                         long long out_rows, int* seqlens_out, float* weights_out,
+                         int* positions_out, long long out_slots, void* workspace,
+                         size_t ws_bytes, fa_stream_t stream);
+
 /* fa_version - library version as major * 10000 + minor * 100 + patch. */
 int fa_version(void);
 

@@ -1,0 +1,420 @@
+"""GPU parity of attention with shaped scores (fwd, bwd, key_ranges), of its decode
+with accumulated weights, and of cache eviction, against the float64 oracle.
+
+Tolerances, element by element, from the roundings that the kernels make. A value
+rounded to bf16 is off by at most 2^-8 of itself. With e the largest error of a
+score z in fp32 (the D products' sums, the cap, the base-2 exponent's rounding) plus
+1e-4 for the exponentials' own error (7.5e-5 at most):
+  O    P rounded to bf16, O rounded:          (2^-8 + 2e) P|V| + 2^-8 |O|
+  LSE                                         e
+  dV   as O:                                  (2^-8 + 2e) P^T|dO| + 2^-8 |dV|
+  dQ   P (once more for dS) and dS rounded, D_i from the rounded O, dQ rounded:
+       (2^-7 + 4e) scale |dX||K| + (2^-8 + 2e) (what D_i moves) + 2^-8 |dQ|;  dK alike.
+       Under a cap 1 - t^2 is formed from a t = tanh that fp32 gives to 2^-22 (a few
+       steps of 2^-24, |t| <= 1), and is off by 2 t 2^-22 + 2^-24 < 2^-20 however small
+       it is: 2^-20 scale |dZ||K| more
+float32: the same without the bf16 terms, e without the 1e-4, and 2^-24 a term summed.
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_tmem_b200 as fa
+from exact_io_aware_tmem_b200.workloads import decode_case, random_case
+from oracle import shaped as osh
+from tests._util import f64
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -8      # half a bf16 step, relative
+# A term below the smallest normal fp32 number (2^-126) has no relative precision: it is
+# off by up to 2^-126, times a factor below 2^7 (|v|, |dO|, |k|, scale), summed over at
+# most 2^12 terms: 2^-107 < 1e-32.
+TINY = 1e-32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from exact_io_aware_tmem_b200 import build
+    build.build()
+
+
+def clean():
+    st, where = fa.check_device_error()
+    assert st == 0, f"device error {st} at {where:#x}"
+
+
+def score_error(q, k, scale, cap, slopes, n, dtype):
+    """Largest error of a score in fp32, plus the exponentials' (see above)."""
+    H, H_kv = q.shape[1], k.shape[1]
+    dot = np.sqrt((f64(q) ** 2).sum(-1).max() * (f64(k) ** 2).sum(-1).max())   # >= sum |q||k|
+    z = min(scale * dot, cap) if cap else scale * dot
+    z += 0.0 if slopes is None else float(slopes.max()) * n
+    e = q.shape[2] * 2.0 ** -24 * scale * dot + 2.0 ** -21 * (2 + z + cap)
+    return e + (1e-4 if dtype == "bf16" else n * 2.0 ** -24)
+
+
+def inside(name, got, ref, tol):
+    got, ref = np.asarray(got), np.asarray(ref)
+    assert np.array_equal(np.isneginf(got), np.isneginf(ref)), f"{name}: -inf rows differ"
+    fin = ~np.isneginf(ref)
+    assert np.isfinite(got[fin]).all(), f"{name}: not finite"
+    over = np.abs(got[fin] - ref[fin]) - (tol if np.isscalar(tol) else tol[fin]) - TINY
+    assert over.size == 0 or over.max() <= 0, f"{name}: {over.max()} outside its bound"
+
+
+def ranges_of(mask, lengths, rng):
+    """(begin, end) of the tokens for a kind of mask, or (None, None)."""
+    if mask == "none":
+        return None, None
+    begin, end = [], []
+    for n in lengths:
+        i = np.arange(n)
+        if mask == "docs":
+            cuts = np.unique(np.concatenate([[0], rng.integers(0, n + 1, 4), [n]]))
+            d = np.searchsorted(cuts, i, side="right")
+            begin.append(cuts[d - 1] if n else i)
+            end.append(cuts[np.minimum(d, len(cuts) - 1)] if n else i)
+        elif mask == "prefix":
+            begin.append(0 * i)
+            end.append(np.maximum(i + 1, int(rng.integers(0, n + 1))))
+        elif mask == "window":
+            begin.append(np.maximum(0, i - int(rng.integers(0, max(1, n // 2)))))
+            end.append(i + 1)
+        else:   # anything: empty rows, entries outside the sequence
+            begin.append(rng.integers(-5, n + 5, n))
+            end.append(rng.integers(-5, n + 9, n))
+    return (np.concatenate(begin).astype(np.int32), np.concatenate(end).astype(np.int32))
+
+
+def run_case(seed, dtype, lengths, H, H_kv, D, varlen, causal, cap, alibi, mask, std=1.0,
+             backward=True, scale=None):
+    inp = random_case(seed, dtype=dtype, lengths=lengths, H=H, H_kv=H_kv, D=D, varlen=varlen,
+                      std=std)
+    B, N = len(lengths), max(lengths)
+    begin, end = ranges_of(mask, lengths, np.random.default_rng(seed))
+    slopes = torch.tensor([0.6 * 0.7 ** h for h in range(H)]) if alibi else None
+    scale = D ** -0.5 if scale is None else scale
+    T = sum(lengths)
+
+    def dev(t):
+        t = t.cuda()
+        return t if varlen else t.view(B, N, *t.shape[1:]).contiguous()
+    q, k, v, do = dev(inp.q), dev(inp.k), dev(inp.v), dev(inp.do)
+    kw = dict(causal=causal, scale=scale, softcap=cap or None,
+              alibi_slopes=None if slopes is None else slopes.cuda(),
+              key_begin=None if begin is None else dev(torch.from_numpy(begin)),
+              key_end=None if end is None else dev(torch.from_numpy(end)))
+    if varlen:
+        kw.update(cu_seqlens=inp.cu_seqlens.cuda(), max_seqlen=N)
+    o, lse = fa.fwd(q, k, v, **kw)
+    clean()
+    ref_args = (inp.cu_seqlens.tolist(), causal, scale, cap, slopes, begin, end)
+    r = osh.forward(inp.q, inp.k, inp.v, *ref_args)
+    e = score_error(inp.q, inp.k, scale, cap, slopes, N, dtype)
+    h = HALF if dtype == "bf16" else 2.0 ** -23
+    lse_ht = f64(lse) if varlen else f64(lse).transpose(1, 0, 2).reshape(H, T)
+    inside("LSE", lse_ht, r.lse, e)
+    inside("O", f64(o).reshape(T, H, D), r.o, (h + 2 * e) * r.o_abs + h * np.abs(r.o))
+    if backward:
+        got = fa.bwd(do, q, k, v, o, lse, **kw)
+        clean()
+        b = osh.backward(inp.q, inp.k, inp.v, inp.do, *ref_args)
+        dq, dk, dv = (f64(x).reshape(y.shape) for x, y in zip(got, (b.dq, b.dk, b.dv)))
+        # 2e also covers the sums of dO V^T and dO.O in fp32, D 2^-24 of their terms.
+        tiny = (e + D * 2.0 ** -23)
+        inside("dV", dv, b.dv, (h + 2 * e) * b.dv_abs + h * np.abs(b.dv))
+        c = 2.0 ** -20 if cap else 0.0
+        inside("dQ", dq, b.dq, c * b.dq_raw + (2 * h + 4 * e) * b.dq_abs + (h + 2 * tiny) * b.dq_del +
+               h * np.abs(b.dq))
+        inside("dK", dk, b.dk, c * b.dk_raw + (2 * h + 4 * e) * b.dk_abs + (h + 2 * tiny) * b.dk_del +
+               h * np.abs(b.dk))
+    return o, lse
+
+
+MASKS = ["none", "docs", "prefix", "window", "any"]
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap,alibi", [(30.0, False), (0.0, True), (5.0, True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bf16_dense(D, cap, alibi, causal, mask):
+    run_case(1 + D, "bf16", [330, 330], 4, 2, D, False, causal, cap, alibi, mask,
+             std=2.0 if cap else 1.0)
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("D,H,H_kv", [(64, 6, 3), (128, 8, 1), (128, 5, 5)])
+def test_bf16_packed(D, H, H_kv, mask):
+    run_case(7 + H, "bf16", [1, 0, 129, 256, 3, 700, 128, 127], H, H_kv, D, True, mask != "prefix",
+             20.0, H != 6, mask, std=1.5)
+
+
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513])
+def test_bf16_lengths(n):
+    for D in (64, 128):
+        run_case(n, "bf16", [n], 2, 1, D, False, True, 50.0, True, "none")
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("D,H,H_kv,n", [(64, 4, 2, 130), (17, 2, 1, 70), (128, 3, 3, 65),
+                                        (1, 1, 1, 33), (40, 4, 1, 1)])
+def test_f32(D, H, H_kv, n, mask):
+    run_case(D, "f32", [n, n], H, H_kv, D, False, mask == "any", 7.0, True, mask)
+
+
+def test_f32_packed():
+    run_case(3, "f32", [5, 0, 90, 1, 33], 4, 2, 32, True, True, 0.0, True, "any")
+
+
+@pytest.mark.parametrize("std,scale", [(1.0, None), (4.0, None), (9.0, 1.0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_cap_far_into_saturation(D, std, scale):
+    # Logits from well inside the cap to many times it; the steep part of tanh
+    # and its flat part both occur.
+    run_case(int(std), "bf16", [200], 2, 2, D, False, True, 10.0, False, "none", std=std,
+             scale=scale)
+
+
+def test_ranges_that_see_nothing():
+    q = torch.randn(2, 200, 4, 64, device="cuda", dtype=torch.bfloat16)
+    z = torch.zeros(2, 200, dtype=torch.int32, device="cuda")
+    o, lse = fa.fwd(q, q, q, key_begin=z, key_end=z)
+    got = fa.bwd(q, q, q, q, o, lse, key_begin=z, key_end=z)
+    clean()
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    assert all((x == 0).all() for x in got)
+
+
+def test_ranges_equal_to_the_plain_masks_give_the_plain_result():
+    # A full range and causal: the same attention by another path.
+    q, k, v = (torch.randn(2, 300, 4, 128, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    z = torch.zeros(2, 300, dtype=torch.int32, device="cuda")
+    o, lse = fa.fwd(q, k, v, causal=True, key_begin=z)
+    o2, lse2 = fa.fwd(q, k, v, causal=True)
+    clean()
+    assert (lse - lse2).abs().max() < 1e-4
+    assert ((o.float() - o2.float()).abs() <= 2 ** -7 * o2.float().abs() + 2 ** -7).all()
+
+
+@pytest.mark.parametrize("window", [0, 1, 7, 5000])
+@pytest.mark.parametrize("docs,prefix", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_key_ranges(causal, docs, prefix, window):
+    if prefix and not causal:
+        return
+    lengths = [1, 0, 5, 1030, 2049]
+    rng = np.random.default_rng(window)
+    ids = (rng.random(sum(lengths)) < 0.02).cumsum().astype(np.int32) if docs else None
+    pre = rng.integers(0, 1500, len(lengths)).astype(np.int32) if prefix else None
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32).cuda()
+    up = lambda a: None if a is None else torch.from_numpy(a).cuda()
+    b, e = fa.key_ranges(sum(lengths), cu_seqlens=cu, max_seqlen=2049, causal=causal,
+                         doc_ids=up(ids), prefix_lens=up(pre), window=window or None)
+    rb, re = osh.key_ranges(lengths, causal, ids, pre, window)
+    clean()
+    assert np.array_equal(b.cpu().numpy(), rb) and np.array_equal(e.cpu().numpy(), re)
+    if docs:   # dense, the same documents
+        d, de = fa.key_ranges(doc_ids=up(ids[6:1036].reshape(2, 515)), causal=causal,
+                              window=window or None)
+        rb, re = osh.key_ranges([515, 515], causal, ids[6:1036], None, window)
+        assert np.array_equal(d.cpu().numpy().ravel(), rb) and np.array_equal(de.cpu().numpy().ravel(), re)
+
+
+# ------------------------------------------------------------------ decode ---
+
+def run_decode(seed, lengths, q_len, H, H_kv, D, page=None, causal=True, cap=0.0, alibi=False,
+               window=0, positions=False, weights=True, std=1.0, max_len=None):
+    c = decode_case(seed, dtype="bf16", lengths=lengths, q_len=q_len, H=H, H_kv=H_kv, D=D,
+                    page_size=page)
+    c.q = c.q * std
+    rng = np.random.default_rng(seed)
+    B, most = len(lengths), max(max(lengths), 1) if max_len is None else max_len
+    slots = most + 3
+    slopes = torch.tensor([0.5 * 0.8 ** h for h in range(H)]) if alibi else None
+    pos = None
+    if positions:
+        pos = np.sort(np.stack([[rng.permutation(2 * slots)[:slots] for _ in range(H_kv)]
+                                for _ in range(B)]), -1).astype(np.int32)
+    w0 = torch.rand(B, H_kv, slots, generator=torch.Generator().manual_seed(seed))
+    w = w0.cuda() if weights else None
+    up = lambda t: None if t is None else t.cuda()
+    if c.block_table is None:
+        c.page_size = c.k_cache.shape[0] // B
+    o, lse = fa.decode(c.q.cuda(), c.k_cache.cuda(), c.v_cache.cuda(), c.cache_seqlens.cuda(),
+                       q_len=q_len, max_seqlen_k=most if page else min(most, c.page_size),
+                       block_table=up(c.block_table), page_size=c.page_size, causal=causal,
+                       softcap=cap or None, alibi_slopes=up(slopes), window=window or None,
+                       key_positions=None if pos is None else torch.from_numpy(pos).cuda(),
+                       key_weights=w)
+    clean()
+    ro, rl, ra, rw = osh.decode(c.q, c.k_cache, c.v_cache, lengths, q_len=q_len, scale=D ** -0.5,
+                                causal=causal, page_size=c.page_size, block_table=c.block_table,
+                                cap=cap, slopes=slopes, window=window, positions=pos, slots=slots)
+    used = torch.isfinite(c.k_cache[:, 0, 0].float())
+    e = score_error(c.q, c.k_cache[used], D ** -0.5, cap, slopes, 2 * slots, "bf16")
+    inside("LSE", f64(lse), rl, e)
+    inside("O", f64(o), ro, (HALF + 2 * e) * ra + HALF * np.abs(ro))
+    if weights:
+        # each weight is exp of a score and an LSE, both off by e, and no bf16
+        inside("weights", f64(w), f64(w0) + rw, 2 * e * rw + 2.0 ** -22 * (1 + rw))
+
+
+LENS = [1, 127, 128, 129, 0, 1000, 255, 256, 2049, 40, 7]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,H,H_kv", [(1, 2, 2), (1, 8, 2), (3, 15, 3), (5, 16, 4), (8, 32, 8),
+                                          (9, 21, 3)])
+def test_decode_rows(q_len, H, H_kv, D):
+    run_decode(q_len * H + D, LENS, q_len, H, H_kv, D, cap=20.0, alibi=H == 8, std=2.0)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [1, 5, 128, 300])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_window(D, window, causal):
+    run_decode(window + D, LENS, 4, 8, 2, D, causal=causal, window=window, alibi=True)
+    run_decode(window + D, LENS, 4, 8, 2, D, causal=causal, window=window, cap=8.0, page=64)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_paged(D, page):
+    run_decode(page + D, LENS, 2, 8, 2, D, page=page, cap=20.0, alibi=True)
+    run_decode(page + D, LENS, 1, 8, 2, D, page=page, alibi=True, weights=False, window=50)
+
+
+@pytest.mark.parametrize("window", [0, 40, 400])
+def test_decode_positions(window):
+    run_decode(window, LENS, 3, 8, 2, 128, positions=True, alibi=True, window=window)
+    run_decode(window, LENS, 1, 4, 4, 64, positions=True, cap=10.0, window=window, page=16)
+
+
+def test_decode_many_sequences_and_few_tiles():
+    rng = np.random.default_rng(5)
+    run_decode(1, [int(x) for x in rng.integers(0, 900, 70)], 1, 8, 4, 128, cap=30.0, alibi=True)
+    run_decode(2, [300, 5, 0, 390], 1, 4, 1, 128, cap=30.0)
+    run_decode(3, [300, 5, 0, 390], 1, 4, 1, 64, alibi=True, window=100)
+    run_decode(4, [1], 1, 1, 1, 64, cap=30.0)
+
+
+def test_decode_max_seqlen_above_the_lengths():
+    run_decode(9, [100, 300], 1, 8, 2, 128, page=64, cap=30.0, max_len=320)
+
+
+# ---------------------------------------------------------------- eviction ---
+
+def run_evict(seed, lengths, H_kv, D, keep, recent, page=None, out_page=None, positions=False,
+              weights=None, out_slots=None):
+    c = decode_case(seed, dtype="bf16", lengths=lengths, q_len=1, H=H_kv, H_kv=H_kv, D=D,
+                    page_size=page)
+    rng = np.random.default_rng(seed)
+    B, most = len(lengths), max(max(lengths), 1)
+    slots = most + 2
+    w = rng.random((B, H_kv, slots)).astype(np.float32) if weights is None else weights(rng, (B, H_kv, slots))
+    pos = rng.integers(0, 1 << 30, (B, H_kv, slots)).astype(np.int32) if positions else None
+    if c.block_table is None:
+        c.page_size = c.k_cache.shape[0] // B
+    kw = {}
+    stride = out_table = None
+    if out_page:
+        n_pages = -(-min(keep, most) // out_page)
+        perm = rng.permutation(B * n_pages + 2)[:B * n_pages].reshape(B, n_pages).astype(np.int32)
+        out_table, rows = perm, (B * n_pages + 2) * out_page
+        kw = dict(out_block_table=torch.from_numpy(perm).cuda(), out_page_size=out_page)
+    else:
+        stride = keep + 1
+        rows = B * stride
+    fill = lambda: torch.full((rows, H_kv, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ko, vo, n_out, w_out, p_out = fa.evict(
+        c.k_cache.cuda(), c.v_cache.cuda(), c.cache_seqlens.cuda(), torch.from_numpy(w).cuda(),
+        keep=keep, recent=recent, max_seqlen_k=most if page else c.page_size,
+        block_table=None if c.block_table is None else c.block_table.cuda(),
+        page_size=c.page_size, key_positions=None if pos is None else torch.from_numpy(pos).cuda(),
+        k_out=fill(), v_out=fill(), out_slots=out_slots, **kw)
+    clean()
+    rk, rv = (torch.full((rows, H_kv, D), 7.0, dtype=torch.bfloat16) for _ in range(2))
+    S = out_slots or keep
+    rw, rp = np.zeros((B, H_kv, S), np.float32), np.full((B, H_kv, S), -1, np.int32)
+    for b, n in enumerate(lengths):
+        at = osh.cache_rows(b, n, c.page_size, c.block_table)
+        for h in range(H_kv):
+            s = osh.kept_slots(w[b, h], n, keep, recent)
+            to = osh.cache_rows(b, len(s), out_page or stride, out_table)
+            rk[to, h], rv[to, h] = c.k_cache[at[s], h], c.v_cache[at[s], h]
+            rw[b, h, :len(s)] = w[b, h, s]
+            rp[b, h, :len(s)] = s if pos is None else pos[b, h, s]
+    assert n_out.cpu().tolist() == [min(n, keep) for n in lengths]
+    assert np.array_equal(p_out.cpu().numpy(), rp)
+    assert np.array_equal(w_out.cpu().numpy(), rw, equal_nan=True)
+    assert torch.equal(ko.cpu(), rk) and torch.equal(vo.cpu(), rv)
+
+
+@pytest.mark.parametrize("keep,recent", [(1, 0), (1, 1), (100, 0), (100, 17), (128, 128), (3000, 5)])
+@pytest.mark.parametrize("D,page,out_page", [(128, None, None), (64, 16, None), (128, 64, 128),
+                                             (64, 256, 16), (8, None, 64)])
+def test_evict(D, page, out_page, keep, recent):
+    run_evict(keep + D, LENS + [2500], 3, D, keep, recent, page, out_page)
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "odd", "tiny"])
+def test_evict_weights_with_ties_and_oddities(kind):
+    def weights(rng, shape):
+        if kind == "equal":
+            return np.full(shape, 0.25, np.float32)
+        if kind == "few":
+            return rng.integers(0, 3, shape).astype(np.float32)
+        if kind == "tiny":
+            return rng.random(shape).astype(np.float32) * 1e-42
+        w = rng.standard_normal(shape).astype(np.float32)
+        w[rng.random(shape) < 0.2] = np.nan
+        w[rng.random(shape) < 0.1] = np.inf
+        w[rng.random(shape) < 0.1] = -np.inf
+        w[rng.random(shape) < 0.1] = -0.0
+        w[rng.random(shape) < 0.1] = 0.0
+        return w
+    for keep, recent in ((200, 0), (200, 33), (1500, 3)):
+        run_evict(4, [2000, 199, 1501, 0, 300], 2, 64, keep, recent, weights=weights)
+
+
+def test_evict_positions_and_room_for_new_tokens():
+    run_evict(8, [700, 30], 2, 128, 100, 10, positions=True, out_slots=160)
+
+
+def test_evict_into_the_same_pool():
+    # 4 pages read, 2 other pages written.
+    pool_k, pool_v = (torch.randn(10 * 64, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    table = torch.tensor([[7, 2, 9, 4]], dtype=torch.int32, device="cuda")
+    out = torch.tensor([[0, 5]], dtype=torch.int32, device="cuda")
+    w = torch.rand(1, 2, 256, device="cuda")
+    old = pool_k.clone()
+    k2, _, n, _, pos = fa.evict(pool_k, pool_v, torch.tensor([250], dtype=torch.int32, device="cuda"),
+                                w, keep=100, recent=8, max_seqlen_k=250, block_table=table,
+                                page_size=64, k_out=pool_k, v_out=pool_v, out_block_table=out,
+                                out_page_size=64)
+    clean()
+    assert k2.data_ptr() == pool_k.data_ptr() and n.item() == 100
+    for h in range(2):
+        s = pos[0, h].long()
+        src = old[table[0].long()[s // 64] * 64 + s % 64, h]
+        i = torch.arange(100, device="cuda")
+        assert torch.equal(pool_k[out[0].long()[i // 64] * 64 + i % 64, h], src)
+    untouched = [7, 2, 9, 4, 1, 3, 6, 8]
+    assert all(torch.equal(pool_k[p * 64:p * 64 + 64], old[p * 64:p * 64 + 64]) for p in untouched)
+
+
+def test_bad_lengths_and_pages_are_reported_not_read():
+    k, v = (torch.randn(2 * 64, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    w = torch.zeros(2, 2, 128, device="cuda")
+    table = torch.tensor([[0, 1], [1, 50]], dtype=torch.int32, device="cuda")
+    for lens in ([128, 129], [-1, 5], [10, 100]):   # too long, negative, page 50 of 2
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        fa.decode(q, k, v, n, q_len=1, max_seqlen_k=128, block_table=table, page_size=64,
+                  softcap=30.0, key_weights=w)
+        assert fa.check_device_error()[0] != 0
+        fa.evict(k, v, n, w, keep=128, recent=0, max_seqlen_k=128, block_table=table, page_size=64)
+        assert fa.check_device_error()[0] != 0
+    clean()
