@@ -65,8 +65,9 @@ fa_status fa_fwd_shaped(const void* q, const void* k, const void* v, void* o, fl
   p.err.word = fa::err_word();
   if (p.err.word == nullptr) return FA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return fa::record_cuda(
-      fa::launch_shaped_fwd_simt(p, fa::shape_args(*shape, p.scale), dtype == FA_F32, s));
+  const fa::ShapeArgs a = fa::shape_args(*shape, p.scale);
+  return fa::record_cuda(dtype == FA_F32 ? fa::launch_shaped_fwd_simt(p, a, true, s)
+                                         : fa::launch_shaped_fwd(p, a, s));
 }
 
 size_t fa_bwd_shaped_workspace_size(long long total_tokens, int B, int H, int D, fa_dtype dtype) {

@@ -1,0 +1,582 @@
+// Attention forward with shaped scores on the sm_100a tensor cores: two 128-row
+// query tiles per CTA, bf16 in, fp32 accumulate, D = 64 or 128.
+//
+//     x_ij = c2 q_i.k_j  or  A tanh(scale q_i.k_j / cap)      (base-2 units)
+//     z_ij = x_ij - slope2 |i - j|,  hidden keys left out,
+// and over key tiles the online softmax: a reference m >= about the row's
+// maximum, l = sum 2^(z - m), O = sum 2^(z - m) V, O / l at the end, LSE =
+// (m + log2 l) ln 2. The reference moves only when a tile's maximum exceeds it
+// by more than 2^8.
+//
+// Which tiles. A query's visible keys are one range [lo, hi). The CTA reduces
+// its rows' ranges to one key-tile range per query tile and walks the union;
+// inside, a warp whose 32 rows see all 128 keys of a tile runs without masks,
+// one that sees none writes zeros.
+//
+// Roles and TMEM are those of the unshaped two-tile kernel: warps 0-3 and 4-7
+// the softmax of query tile 0 and 1 (thread = row), warp 8 TMA, warp 9 MMA;
+// S_g [128 g, 128 g + 128) with P_g as bf16 over its first 64 columns, O_g
+// from 256 on. What differs is how the softmax reads S: twice, 32 columns at a
+// time (once for the maximum, once for the exponentials), instead of holding
+// all 128 scores. The cap costs nine instructions a score against the plain
+// path's three and a half; with 32 live scores its loop is small enough to
+// stay in the instruction cache in all its forms and nothing spills.
+//
+// The cap. Up to |s| <= cap / scale (|tanh| <= 0.76) a polynomial on packed
+// fp32 pairs (score_cap.cuh), which leaves the special-function unit to the one
+// exponential a score; a warp whose tile holds a larger score takes tanh by
+// exponential and reciprocal for that tile.
+//
+// The bias. Along a row |i - j| slope2 is linear on either side of the
+// diagonal: one fused multiply-add a score. The maximum then comes from the
+// unbiased scores plus the tile's least distance, an upper bound that exceeds
+// the true maximum by 127 slope2 at most, as long as that is below 2^100's
+// exponent (the sums stay normal numbers); steeper slopes compute the biased
+// scores in the first reading too.
+#include <limits.h>
+#include <math.h>
+
+#include "score_cap.cuh"
+#include "shaped.h"
+
+namespace fa {
+namespace {
+namespace sfwd {
+
+constexpr int BM = 128;
+constexpr int BN = 128;
+constexpr int THREADS = 320;
+constexpr int WARP_TMA = 8;
+constexpr int WARP_MMA = 9;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_S = 0;
+constexpr uint32_t TM_O = 256;
+constexpr uint32_t SPAN = 128 * 128;
+constexpr float RESCALE_LOG2 = 8.f;
+constexpr float BOUND_LOG2 = 100.f;   // largest excess of the bound over a row's maximum
+constexpr unsigned FULL = 0xffffffffu;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t TILE = BM * D * 2;
+  static constexpr int KS = D == 128 ? 3 : 4;
+  static constexpr int VS = D == 128 ? 2 : 4;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + KS * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + VS * TILE;
+  // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2],
+  // p_ready[2], o_full
+  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 5;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;   // tmem slot, abort, lo[2], hi[2]
+  static constexpr uint32_t SMEM = OFF_MISC + 32;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+template <int D>
+struct Bars {
+  using C = Cfg<D>;
+  uint32_t b;
+  __device__ uint32_t q_full() const { return b; }
+  __device__ uint32_t k_full(int s) const { return b + 8u * (1 + s); }
+  __device__ uint32_t k_empty(int s) const { return b + 8u * (1 + C::KS + s); }
+  __device__ uint32_t v_full(int s) const { return b + 8u * (1 + 2 * C::KS + s); }
+  __device__ uint32_t v_empty(int s) const { return b + 8u * (1 + 2 * C::KS + C::VS + s); }
+  __device__ uint32_t s_full(int g) const { return b + 8u * (1 + 2 * C::KS + 2 * C::VS + g); }
+  __device__ uint32_t p_ready(int g) const { return b + 8u * (3 + 2 * C::KS + 2 * C::VS + g); }
+  __device__ uint32_t o_full() const { return b + 8u * (5 + 2 * C::KS + 2 * C::VS); }
+};
+
+enum : unsigned {
+  W_Q = 0xC0100, W_KEMPTY = 0xC0200, W_VEMPTY = 0xC0300, W_KFULL = 0xC0400, W_VFULL = 0xC0500,
+  W_SFULL = 0xC0600, W_PREADY = 0xC0700, W_OFULL = 0xC0800, BAD_ALIGN = 0xC0900
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const DevErr& e,
+                                          volatile int* abort, unsigned where) {
+  const bool ok = mbar_wait(bar, parity, e, abort, where);
+  return __all_sync(FULL, ok);
+}
+
+__device__ __forceinline__ float pair_max(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// What a row's thread knows of one tile.
+struct RowTile {
+  int lo, hi;   // visible columns [lo, hi) of the tile
+  int dist0;    // first key - query
+};
+
+// First reading: the tile's (bound on the) maximum of this row's visible z.
+// big: some score of the warp's tile is outside the polynomial's range.
+template <bool CAP, bool BIAS, bool PARTIAL>
+__device__ __forceinline__ float tile_max(uint32_t s_col, const RowTile& t, float c2,
+                                          const CapArgs& cap, float slope2, bool steep, bool& big) {
+  float mx[2] = {-INFINITY, -INFINITY}, ab[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(s_col + 32 * c, r);
+    tmem_ld_wait();
+    reg_fence(r);
+    if (BIAS && steep) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float s = __uint_as_float(r[i]);
+        float z = CAP ? cap_exact(cap, s) : s * c2;
+        z = fmaf(-slope2, fabsf(static_cast<float>(t.dist0 + 32 * c + i)), z);
+        if (!PARTIAL || (32 * c + i >= t.lo && 32 * c + i < t.hi)) mx[i & 1] = fmaxf(mx[i & 1], z);
+        if (CAP) ab[i & 1] = fmaxf(ab[i & 1], fabsf(s));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          s[u] = __uint_as_float(r[i + u]);
+          if (CAP) ab[u >> 1] = fmaxf(ab[u >> 1], fabsf(s[u]));
+          if (PARTIAL && !(32 * c + i + u >= t.lo && 32 * c + i + u < t.hi)) s[u] = -INFINITY;
+        }
+        mx[0] = pair_max(mx[0], s[0], s[1]);
+        mx[1] = pair_max(mx[1], s[2], s[3]);
+      }
+    }
+  }
+  const float m = fmaxf(mx[0], mx[1]);
+  if (CAP) big = __any_sync(FULL, fmaxf(ab[0], ab[1]) > cap.limit);
+  if (BIAS && steep) return m;
+  float x = CAP ? cap_exact(cap, m) : m * c2;
+  if (CAP && m == -INFINITY) x = -INFINITY;
+  // The key nearest to the query: distance 0, or that of the tile's nearer end.
+  if (BIAS) x -= slope2 * static_cast<float>(max(0, max(t.dist0, -(t.dist0 + BN - 1))));
+  return x;
+}
+
+// Second reading: P = 2^(z - m) as bf16 over the first 64 columns of S; returns the row's sum.
+template <bool CAP, bool BIAS, bool PARTIAL, bool BIG>
+__device__ __forceinline__ float tile_exp(uint32_t s_col, const RowTile& t, float c2,
+                                          const CapArgs& cap, float slope2, float m) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  // Bias along the row: sl (column) + off, sl of either sign. Where a chunk
+  // holds the diagonal the distance is taken per element.
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(s_col + 32 * c, r);
+    tmem_ld_wait();
+    reg_fence(r);
+    const int d0 = t.dist0 + 32 * c;          // first key of the chunk - query
+    const bool right = d0 >= 0;
+    const float sl = right ? -slope2 : slope2;
+    const bool mixed = PARTIAL && BIAS && __any_sync(FULL, d0 < 0 && d0 + 31 > 0);
+    const float base = BIAS ? fmaf(sl, static_cast<float>(d0), -m) : -m;
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 s = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+      float2 add = make_float2(base, base);
+      if (BIAS) {
+        if (mixed) {
+          add.x = fmaf(-slope2, fabsf(static_cast<float>(d0 + i)), -m);
+          add.y = fmaf(-slope2, fabsf(static_cast<float>(d0 + i + 1)), -m);
+        } else {
+          add = __ffma2_rn(make_float2(sl, sl), make_float2(static_cast<float>(i), static_cast<float>(i + 1)),
+                           add);
+        }
+      }
+      float2 x;
+      if (!CAP)
+        x = __ffma2_rn(s, make_float2(c2, c2), add);
+      else if (!BIG)
+        x = cap_poly2(cap, s, add);
+      else
+        x = make_float2(fmaf(cap.amp, cap_tanh(cap, s.x), add.x), fmaf(cap.amp, cap_tanh(cap, s.y), add.y));
+      float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+      if (PARTIAL) {
+        const int j = 32 * c + i;
+        p0 = (j >= t.lo && j < t.hi) ? p0 : 0.f;
+        p1 = (j + 1 >= t.lo && j + 1 < t.hi) ? p1 : 0.f;
+      }
+      sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], make_float2(p0, p1));
+      pk[i >> 1] = pack_bf16x2(p0, p1);
+    }
+    // Columns 16 c .. 16 c + 15: scores of chunk c / 2, read already.
+    tmem_st16(s_col + 16 * c, pk);
+  }
+  return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(THREADS, 1)
+    shaped_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const AttnParams p,
+                      const ShapeArgs sh, const CapArgs cap, int num_m2, int group) {
+  using C = Cfg<D>;
+  constexpr int KS = C::KS, VS = C::VS;
+  constexpr uint32_t TILE = C::TILE, OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if ((sbase & 1023u) != 0) {
+    if (threadIdx.x == 0) record_bounds(p.err, BAD_ALIGN);
+    return;
+  }
+  // Groups of heads for L2 reuse of K / V; inside a group the last query tiles
+  // (the longest under a causal mask) first.
+  const TileSlot ts = grouped_slot(blockIdx.x, num_m2, p.H * p.B, group);
+  const int m2 = num_m2 - 1 - ts.t;
+  const int h = ts.unit % p.H;
+  const int b = ts.unit / p.H;
+  const SeqInfo sq = seq_info(p, b);
+  if (!seq_ok(p, sq) || m2 * 2 * BM >= sq.len) return;   // whole CTA, before any shared state
+  const int hk = h / (p.H / p.H_kv);
+
+  const Bars<D> bars{sbase + C::OFF_BAR};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* s_lo = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);    // per query tile
+  int* s_hi = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+
+  // This thread's row (softmax warps) and its keys.
+  const int qpos = (m2 * 2 + (warp >> 2)) * BM + (warp & 3) * 32 + lane;
+  KeyRange kr = {0, 0};
+  if (warp < 8 && qpos < sq.len) kr = key_range(p, sh, sq, qpos);
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    s_lo[0] = s_lo[1] = INT_MAX;
+    s_hi[0] = s_hi[1] = 0;
+    mbar_init(bars.q_full(), 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(bars.k_full(s), 1);
+      mbar_init(bars.k_empty(s), 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(bars.v_full(s), 1);
+      mbar_init(bars.v_empty(s), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bars.s_full(g), 1);
+      mbar_init(bars.p_ready(g), 128);
+    }
+    mbar_init(bars.o_full(), 1);
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp < 8) {
+    const int lo = __reduce_min_sync(FULL, kr.lo < kr.hi ? kr.lo : INT_MAX);
+    const int hi = __reduce_max_sync(FULL, kr.hi);
+    if (lane == 0 && hi > 0) {
+      atomicMin(&s_lo[warp >> 2], lo);
+      atomicMax(&s_hi[warp >> 2], hi);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Key tiles [t_g, t_g + n_g) of query tile g; the CTA walks [t0, t0 + n_kv),
+  // step it of it is key tile t0 + it, and tile g takes part from step s_g on.
+  const int t_0 = s_hi[0] > 0 ? s_lo[0] / BN : INT_MAX, t_1 = s_hi[1] > 0 ? s_lo[1] / BN : INT_MAX;
+  const int e_0 = (s_hi[0] + BN - 1) / BN, e_1 = (s_hi[1] + BN - 1) / BN;
+  const int t0 = min(t_0, t_1);
+  const int n_kv = t0 == INT_MAX ? 0 : max(e_0, e_1) - t0;
+  // Steps [b_g, f_g) of tile g; empty when it sees nothing.
+  const int b_0 = t_0 == INT_MAX ? 0 : t_0 - t0, f_0 = t_0 == INT_MAX ? 0 : e_0 - t0;
+  const int b_1 = t_1 == INT_MAX ? 0 : t_1 - t0, f_1 = t_1 == INT_MAX ? 0 : e_1 - t0;
+
+  if (warp == WARP_TMA) {
+    // ------------------------------------------------------------ producer ---
+    // The whole warp runs the loop; lane 0 issues the copies.
+    if (lane == 0 && n_kv > 0) {
+      mbar_arrive_expect_tx(bars.q_full(), 2 * TILE);
+      for (int g = 0; g < 2; ++g)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_2d(sbase + OFF_Q + g * TILE + c * SPAN, &tm_q, bars.q_full(), h * D + c * 64,
+                      sq.start + (2 * m2 + g) * BM);
+    }
+    int jk = 0, jv = 0;
+    long long t_last = clock64();
+    while (jk < n_kv || jv < n_kv) {
+      bool progress = false;
+      if (jk < n_kv &&
+          __all_sync(FULL, mbar_try_wait(bars.k_empty(jk % KS), ((jk / KS) & 1) ^ 1))) {
+        const int st = jk % KS;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bars.k_full(st), TILE);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_2d(sbase + OFF_K + st * TILE + c * SPAN, &tm_k, bars.k_full(st),
+                        hk * D + c * 64, sq.start + (t0 + jk) * BN);
+        }
+        __syncwarp();
+        ++jk;
+        progress = true;
+      }
+      if (jv < jk &&
+          __all_sync(FULL, mbar_try_wait(bars.v_empty(jv % VS), ((jv / VS) & 1) ^ 1))) {
+        const int st = jv % VS;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bars.v_full(st), TILE);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_2d(sbase + OFF_V + st * TILE + c * SPAN, &tm_v, bars.v_full(st),
+                        hk * D + c * 64, sq.start + (t0 + jv) * BN);
+        }
+        __syncwarp();
+        ++jv;
+        progress = true;
+      }
+      if (progress) {
+        t_last = clock64();
+        continue;
+      }
+      // Lane 0 decides, so the whole warp leaves the loop together.
+      const int stop =
+          __shfl_sync(FULL, *abort ? 1 : (clock64() - t_last > p.err.budget ? 2 : 0), 0);
+      if (stop == 1) break;
+      if (stop == 2) {
+        if (lane == 0) {
+          *abort = 1;
+          atomicOr(p.err.word, ERR_TIMEOUT);
+          atomicExch(p.err.word + 1, jk < n_kv ? W_KEMPTY : W_VEMPTY);
+        }
+        break;
+      }
+    }
+    if (lane == 0) {
+      // Drain: the tensor core's arrivals on the last stages' empty barriers
+      // must land before the CTA's shared memory is released.
+      for (int j = max(0, n_kv - KS); j < n_kv && !*abort; ++j)
+        if (!mbar_wait(bars.k_empty(j % KS), (j / KS) & 1, p.err, abort, W_KEMPTY)) break;
+      for (int j = max(0, n_kv - VS); j < n_kv && !*abort; ++j)
+        if (!mbar_wait(bars.v_empty(j % VS), (j / VS) & 1, p.err, abort, W_VEMPTY)) break;
+    }
+  } else if (warp == WARP_MMA) {
+    // ---------------------------------------------------------- MMA issuer ---
+    // Per step: P_0 V, S_0 of the next, P_1 V, S_1 of the next, for the tiles
+    // that take part. S_g of the next step overwrites P_g: it follows P_g V.
+    const uint32_t leader = elect_one();
+    constexpr uint32_t IDESC_QK = idesc_bf16(BM, BN, false, false);
+    constexpr uint32_t IDESC_PV = idesc_bf16(BM, D, false, true);
+    const uint64_t q_desc = sdesc_sw128(sbase + OFF_Q, 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(sbase + OFF_K, 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(sbase + OFF_V, SPAN, 1024);
+    auto issue_s = [&](int g, int it) {
+      const int st = it % KS;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * SPAN + (kk & 3) * 32;
+        mma_ss_if(leader, tmem + TM_S + g * BN, sdesc_add(q_desc, g * TILE + o),
+                  sdesc_add(k_desc, st * TILE + o), IDESC_QK, kk > 0);
+      }
+      tc_commit_if(leader, bars.s_full(g));
+    };
+    auto issue_pv = [&](int g, int it, bool fresh) {
+      const int st = it % VS;
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+        mma_ts_if(leader, tmem + TM_O + g * D, tmem + TM_S + g * BN + kk * 8,
+                  sdesc_add(v_desc, st * TILE + kk * 2048), IDESC_PV,
+                  (!fresh || kk > 0) ? 1u : 0u);
+    };
+    bool ok = n_kv > 0;
+    if (ok) {
+      ok = warp_wait(bars.q_full(), 0, p.err, abort, W_Q) &&
+           warp_wait(bars.k_full(0), 0, p.err, abort, W_KFULL);
+      if (ok) {
+        tc_fence_after();
+        if (b_0 == 0 && f_0 > 0) issue_s(0, 0);
+        if (b_1 == 0 && f_1 > 0) issue_s(1, 0);
+        tc_commit_if(leader, bars.k_empty(0));
+      }
+    }
+    for (int it = 0; ok && it < n_kv; ++it) {
+      const bool next = it + 1 < n_kv;
+      if (!(ok = warp_wait(bars.v_full(it % VS), (it / VS) & 1, p.err, abort, W_VFULL))) break;
+      bool k_seen = false;
+#pragma unroll
+      for (int g = 0; g < 2 && ok; ++g) {
+        const int bg = g ? b_1 : b_0, fg = g ? f_1 : f_0;
+        if (it >= bg && it < fg) {
+          if (!(ok = warp_wait(bars.p_ready(g), (it - bg) & 1, p.err, abort, W_PREADY))) break;
+          tc_fence_after();
+          issue_pv(g, it, it == bg);
+        }
+        if (it + 1 >= bg && it + 1 < fg) {
+          if (!k_seen) {
+            if (!(ok = warp_wait(bars.k_full((it + 1) % KS), ((it + 1) / KS) & 1, p.err, abort,
+                                 W_KFULL)))
+              break;
+            tc_fence_after();
+            k_seen = true;
+          }
+          issue_s(g, it + 1);
+        }
+      }
+      if (!ok) break;
+      tc_commit_if(leader, bars.v_empty(it % VS));
+      if (next) {
+        // A tile between the two ranges is read by neither: its stage is given
+        // back once it has landed.
+        if (!k_seen && !(ok = warp_wait(bars.k_full((it + 1) % KS), ((it + 1) / KS) & 1, p.err,
+                                        abort, W_KFULL)))
+          break;
+        tc_commit_if(leader, bars.k_empty((it + 1) % KS));
+      }
+    }
+    if (n_kv > 0) tc_commit_if(leader, bars.o_full());   // some softmax group waits for it
+  } else {
+    // ------------------------------------------------------------- softmax ---
+    const int g = warp >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + TM_S + g * BN;
+    const uint32_t o_col = tmem + lane_off + TM_O + g * D;
+    const int bg = g ? b_1 : b_0, n = (g ? f_1 : f_0) - bg;
+    const float c2 = p.scale_log2;
+    const float slope2 = BIAS ? __ldg(sh.slopes + h) * LOG2E : 0.f;
+    const bool steep = BIAS && fabsf(slope2) * 127.f > BOUND_LOG2;
+    float m_ref = -INFINITY;
+    float l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      const int key0 = (t0 + bg + i) * BN;
+      RowTile t;
+      t.lo = kr.lo - key0;
+      t.hi = kr.hi - key0;
+      t.dist0 = key0 - qpos;
+      // A warp that sees the whole tile on one side of the diagonal needs no
+      // element-wise mask or distance.
+      const bool whole = __all_sync(FULL, t.lo <= 0 && t.hi >= BN &&
+                                              (!BIAS || t.dist0 >= 0 || t.dist0 + BN <= 1));
+      const bool none = !whole && !__any_sync(FULL, t.lo < BN && t.hi > 0 && t.lo < t.hi);
+      if (!(ok = warp_wait(bars.s_full(g), i & 1, p.err, abort, W_SFULL))) break;
+      tc_fence_after();
+      float alpha = 1.f;
+      if (none) {
+        const uint32_t z[16] = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(s_col + 16 * c, z);
+      } else {
+        bool big = false;
+        const float m_cand =
+            whole ? tile_max<CAP, BIAS, false>(s_col, t, c2, cap, slope2, steep, big)
+                  : tile_max<CAP, BIAS, true>(s_col, t, c2, cap, slope2, steep, big);
+        const bool grow = m_cand > m_ref + RESCALE_LOG2;   // always true on the first visible tile
+        const float m_new = grow ? m_cand : m_ref;
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        float sum;
+        if (CAP && big)
+          sum = whole ? tile_exp<CAP, BIAS, false, CAP>(s_col, t, c2, cap, slope2, m_use)
+                      : tile_exp<CAP, BIAS, true, CAP>(s_col, t, c2, cap, slope2, m_use);
+        else
+          sum = whole ? tile_exp<CAP, BIAS, false, false>(s_col, t, c2, cap, slope2, m_use)
+                      : tile_exp<CAP, BIAS, true, false>(s_col, t, c2, cap, slope2, m_use);
+        if (grow && m_ref != -INFINITY) alpha = ex2_approx(m_ref - m_use);
+        l = l * alpha + sum;
+        m_ref = m_new;
+      }
+      // The reference moved: O, which holds the earlier tiles only (S_g of this
+      // step completing means P_g V of the previous one has), moves with it.
+      if (i > 0 && __any_sync(FULL, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_ld_wait();
+          reg_fence(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(o_col + 32 * c, o);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bars.p_ready(g));
+    }
+    // ------------------------------------------------------------ epilogue ---
+    const bool row_ok = qpos < sq.len;
+    const size_t out_row = static_cast<size_t>(sq.start + qpos) * p.H + h;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D);
+    if (n > 0) ok = ok && warp_wait(bars.o_full(), 0, p.err, abort, W_OFULL);
+    if (ok) {
+      tc_fence_after();
+      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_ld_wait();
+          reg_fence(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (row_ok) {
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[8 * v4 + 0]) * inv_l, __uint_as_float(o[8 * v4 + 1]) * inv_l);
+            w.y = pack_bf16x2(__uint_as_float(o[8 * v4 + 2]) * inv_l, __uint_as_float(o[8 * v4 + 3]) * inv_l);
+            w.z = pack_bf16x2(__uint_as_float(o[8 * v4 + 4]) * inv_l, __uint_as_float(o[8 * v4 + 5]) * inv_l);
+            w.w = pack_bf16x2(__uint_as_float(o[8 * v4 + 6]) * inv_l, __uint_as_float(o[8 * v4 + 7]) * inv_l);
+            dst[4 * c + v4] = w;
+          }
+        }
+      }
+      if (row_ok)
+        p.lse[lse_index(p, b, h, sq.start, qpos)] =
+            (l > 0.f) ? (m_ref + __log2f(l)) * LN2 : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <int D, bool CAP, bool BIAS>
+cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const int num_m2 = (p.max_seqlen + 2 * BM - 1) / (2 * BM);
+  const long long tiles = static_cast<long long>(num_m2) * p.H * p.B;
+  if (tiles > INT_MAX) return cudaErrorInvalidConfiguration;
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_bf16_2d(&tq, p.q, p.total, static_cast<unsigned long long>(p.H) * D, 64, BM) ||
+      !make_tmap_bf16_2d(&tk, p.k, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN) ||
+      !make_tmap_bf16_2d(&tv, p.v, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(shaped_fwd_kernel<D, CAP, BIAS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int group = l2_group(4ll * p.max_seqlen * D, p.H / p.H_kv, p.H * p.B);
+  const CapArgs cap = CAP ? cap_args(sh.cap, p.scale) : CapArgs{};
+  shaped_fwd_kernel<D, CAP, BIAS><<<static_cast<unsigned>(tiles), THREADS, C::SMEM, stream>>>(
+      tq, tk, tv, p, sh, cap, num_m2, group);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
+  const bool cap = sh.cap > 0.f, bias = sh.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true>(p, sh, stream) : launch<D, true, false>(p, sh, stream);
+  return bias ? launch<D, false, true>(p, sh, stream) : launch<D, false, false>(p, sh, stream);
+}
+
+}  // namespace sfwd
+}  // namespace
+
+cudaError_t launch_shaped_fwd(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
+  return p.D == 64 ? sfwd::launch_d<64>(p, sh, stream) : sfwd::launch_d<128>(p, sh, stream);
+}
+
+}  // namespace fa
