@@ -100,6 +100,11 @@ cudaError_t launch_shaped_bwd_simt(const AttnParams& p, const ShapeArgs& sh, boo
                                    cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_fwd.cu).
 cudaError_t launch_shaped_fwd(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
+// bf16, D = 64 or 128 (shaped_bwd.cu): p.delta and p.dq_accum as for the fused
+// backward, ``tiles`` shaped_bwd_tiles_bytes() of scratch.
+size_t shaped_bwd_tiles_bytes(long long total, int B);
+cudaError_t launch_shaped_bwd(const AttnParams& p, const ShapeArgs& sh, void* tiles,
+                              cudaStream_t stream);
 cudaError_t launch_key_ranges(const AttnParams& p, const int* doc_ids, const int* prefix_lens,
                               int window, int* key_begin, int* key_end, cudaStream_t stream);
 cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,

@@ -71,8 +71,9 @@ fa_status fa_fwd_shaped(const void* q, const void* k, const void* v, void* o, fl
 }
 
 size_t fa_bwd_shaped_workspace_size(long long total_tokens, int B, int H, int D, fa_dtype dtype) {
-  if (B < 0) return 0;
-  return fa_bwd_workspace_size(total_tokens, H, D, dtype);
+  const size_t base = fa_bwd_workspace_size(total_tokens, H, D, dtype);
+  if (B < 0 || base == 0) return 0;
+  return base + (dtype == FA_BF16 ? fa::round256(fa::shaped_bwd_tiles_bytes(total_tokens, B)) : 0);
 }
 
 fa_status fa_bwd_shaped(const void* q, const void* k, const void* v, const void* o,
@@ -106,12 +107,19 @@ fa_status fa_bwd_shaped(const void* q, const void* k, const void* v, const void*
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
-  p.delta = static_cast<float*>(workspace);
+  char* ws = static_cast<char*>(workspace);
+  p.delta = reinterpret_cast<float*>(ws);
   p.err.word = fa::err_word();
   if (p.err.word == nullptr) return FA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return fa::record_cuda(
-      fa::launch_shaped_bwd_simt(p, fa::shape_args(*shape, p.scale), dtype == FA_F32, s));
+  const fa::ShapeArgs a = fa::shape_args(*shape, p.scale);
+  if (dtype == FA_F32) return fa::record_cuda(fa::launch_shaped_bwd_simt(p, a, true, s));
+  // D_i, the dQ accumulator, the query tiles' ranges.
+  const size_t rows = static_cast<size_t>(p.total) * H;
+  ws += fa::round256(rows * sizeof(float));
+  p.dq_accum = reinterpret_cast<float*>(ws);
+  ws += fa::round256(rows * D * sizeof(float));
+  return fa::record_cuda(fa::launch_shaped_bwd(p, a, ws, s));
 }
 
 fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, int causal, int B,

@@ -75,6 +75,8 @@ class Backward:
     dk_del: np.ndarray
     dq_raw: np.ndarray   # scale |dZ| |K|: what an error of the cap's derivative moves
     dk_raw: np.ndarray
+    dq_one: np.ndarray   # scale |dO V^T - D| |K| over the visible keys: what an absolute
+    dk_one: np.ndarray   # error of P moves
 
 
 def _heads(q, k, v, cu, causal, scale, cap, slopes, begin, end):
@@ -110,12 +112,14 @@ def forward(q, k, v, cu, causal, scale, cap=0.0, slopes=None, begin=None, end=No
 def backward(q, k, v, do, cu, causal, scale, cap=0.0, slopes=None, begin=None,
              end=None) -> Backward:
     g = _f64(do)
-    r = Backward(*(np.zeros(_f64(x).shape) for x in (q, k, k, q, k, k, q, k, q, k)))
+    r = Backward(*(np.zeros(_f64(x).shape) for x in (q, k, k, q, k, k, q, k, q, k, q, k)))
     for rows, h, hk, p, _, grad, qq, kk, vv in _heads(q, k, v, cu, causal, scale, cap, slopes,
                                                       begin, end):
         d = g[rows, h]
         o = p @ vv
-        dz = p * (d @ vv.T - (d * o).sum(1, keepdims=True))
+        dp = d @ vv.T - (d * o).sum(1, keepdims=True)
+        dz = p * dp
+        dp = np.abs(dp) * (p > 0)
         dx = dz * grad
         r.dq[rows, h] += scale * dx @ kk
         r.dk[rows, hk] += scale * dx.T @ qq
@@ -128,6 +132,8 @@ def backward(q, k, v, do, cu, causal, scale, cap=0.0, slopes=None, begin=None,
         r.dk_del[rows, hk] += scale * de.T @ np.abs(qq)
         r.dq_raw[rows, h] += scale * np.abs(dz) @ np.abs(kk)
         r.dk_raw[rows, hk] += scale * np.abs(dz).T @ np.abs(qq)
+        r.dq_one[rows, h] += scale * dp @ np.abs(kk)
+        r.dk_one[rows, hk] += scale * dp.T @ np.abs(qq)
     return r
 
 

@@ -12,7 +12,9 @@ score z in fp32 (the D products' sums, the cap, the base-2 exponent's rounding) 
        (2^-7 + 4e) scale |dX||K| + (2^-8 + 2e) (what D_i moves) + 2^-8 |dQ|;  dK alike.
        Under a cap 1 - t^2 is formed from a t = tanh that fp32 gives to 2^-22 (a few
        steps of 2^-24, |t| <= 1), and is off by 2 t 2^-22 + 2^-24 < 2^-20 however small
-       it is: 2^-20 scale |dZ||K| more
+       it is: 2^-20 scale |dZ||K| more.
+       P (1 - t^2) 2^14 is held as fp16 for dX: its step below 2^-14 is 2^-24, so P (1 - t^2)
+       is off by up to 2^-25 2^-14 = 2^-39 however small it is: 2^-39 scale |dO V^T - D||K| more
 float32: the same without the bf16 terms, e without the 1e-4, and 2^-24 a term summed.
 """
 import numpy as np
@@ -125,9 +127,10 @@ def run_case(seed, dtype, lengths, H, H_kv, D, varlen, causal, cap, alibi, mask,
         tiny = (e + D * 2.0 ** -23)
         inside("dV", dv, b.dv, (h + 2 * e) * b.dv_abs + h * np.abs(b.dv))
         c = 2.0 ** -20 if cap else 0.0
-        inside("dQ", dq, b.dq, c * b.dq_raw + (2 * h + 4 * e) * b.dq_abs + (h + 2 * tiny) * b.dq_del +
+        f = 2.0 ** -39 if dtype == "bf16" else 0.0
+        inside("dQ", dq, b.dq, f * b.dq_one + c * b.dq_raw + (2 * h + 4 * e) * b.dq_abs + (h + 2 * tiny) * b.dq_del +
                h * np.abs(b.dq))
-        inside("dK", dk, b.dk, c * b.dk_raw + (2 * h + 4 * e) * b.dk_abs + (h + 2 * tiny) * b.dk_del +
+        inside("dK", dk, b.dk, f * b.dk_one + c * b.dk_raw + (2 * h + 4 * e) * b.dk_abs + (h + 2 * tiny) * b.dk_del +
                h * np.abs(b.dk))
     return o, lse
 
