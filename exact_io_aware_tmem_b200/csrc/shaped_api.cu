@@ -141,8 +141,9 @@ fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, 
 size_t fa_decode_shaped_workspace_size(int B, int q_len, int H, int H_kv, int D, int max_seqlen_k,
                                        int weights) {
   if (B <= 0 || q_len <= 0 || H <= 0 || H_kv <= 0 || D <= 0 || max_seqlen_k < 0) return 0;
-  (void)weights;
-  return 0;
+  const long long rows = static_cast<long long>(q_len) * (H / H_kv);
+  if (H % H_kv != 0 || rows > 64) return 0;
+  return fa::decode_shaped_workspace(B, H_kv, rows, D, max_seqlen_k, weights != 0);
 }
 
 fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cache, void* o,
@@ -178,7 +179,7 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
   a.key_weights = shape->key_weights;
   a.slots = shape->slots;
   return fa::record_cuda(
-      fa::launch_decode_shaped(p, d, a, reinterpret_cast<cudaStream_t>(stream)));
+      fa::launch_decode_shaped(p, d, a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t fa_cache_evict_workspace_size(int B, int H_kv, int keep) {
