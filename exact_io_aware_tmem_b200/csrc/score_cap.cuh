@@ -19,32 +19,23 @@ constexpr double CAP_C[CAP_TERMS] = {0.9999997019767761,   -0.3333212733268738,
                                      0.019972829148173332, -0.005950915161520243,
                                      0.0009636600152589381};
 
-// By value to the kernels. poly[i] = A (scale / cap)^(2 i + 1) C[i], so that the
-// polynomial runs on s itself; it holds for |s| <= limit.
+// By value to the kernels.
 struct CapArgs {
-  float poly[CAP_TERMS];
-  float tpoly[CAP_TERMS];   // the same without A: tanh itself
-  float limit;              // cap / scale, or -1: always the exponential form
+  float poly[CAP_TERMS];    // A C[i]
+  float c1;                 // scale / cap: u = c1 s
+  float limit;              // 1 / c1: the polynomial holds for |s| <= limit
   float amp;                // A
-  float k2;                 // 2 log2 e scale / cap: e^(2u) = 2^(k2 s)
+  float k2;                 // 2 log2 e c1: e^(2u) = 2^(k2 s)
 };
 
 inline CapArgs cap_args(float cap, float scale) {
   CapArgs a = {};
   const double log2e = 1.4426950408889634, c1 = static_cast<double>(scale) / cap;
   a.amp = static_cast<float>(cap * log2e);
+  a.c1 = static_cast<float>(c1);
   a.k2 = static_cast<float>(2.0 * log2e * c1);
   a.limit = static_cast<float>(1.0 / c1);
-  double pw = c1;
-  for (int i = 0; i < CAP_TERMS; ++i, pw *= c1 * c1) {
-    a.poly[i] = static_cast<float>(cap * log2e * pw * CAP_C[i]);
-    a.tpoly[i] = static_cast<float>(pw * CAP_C[i]);
-    // Powers of an extreme scale / cap that leave fp32's normal range (both
-    // ways) leave the polynomial without its terms.
-    const double least = fmin(fabs(a.poly[i]), fabs(a.tpoly[i]));
-    if (!isfinite(a.poly[i]) || !isfinite(a.tpoly[i]) || least < 1e-37) a.limit = -1.f;
-  }
-  if (!isfinite(a.limit)) a.limit = -1.f;
+  for (int i = 0; i < CAP_TERMS; ++i) a.poly[i] = static_cast<float>(cap * log2e * CAP_C[i]);
   return a;
 }
 
@@ -64,14 +55,26 @@ __device__ __forceinline__ float cap_exact(const CapArgs& a, float s) {
   return a.amp * cap_tanh(a, s);
 }
 
-// Two scores within the limit, on packed fp32 pairs: x + add.
+// Two scores within the limit, on packed fp32 pairs: A tanh + add.
 __device__ __forceinline__ float2 cap_poly2(const CapArgs& a, float2 s, float2 add) {
-  const float2 w = __fmul2_rn(s, s);
+  const float2 u = __fmul2_rn(s, make_float2(a.c1, a.c1));
+  const float2 w = __fmul2_rn(u, u);
   float2 t = make_float2(a.poly[CAP_TERMS - 1], a.poly[CAP_TERMS - 1]);
 #pragma unroll
   for (int i = CAP_TERMS - 2; i >= 0; --i)
     t = __ffma2_rn(t, w, make_float2(a.poly[i], a.poly[i]));
-  return __ffma2_rn(s, t, add);
+  return __ffma2_rn(u, t, add);
+}
+
+// The same without A and add: tanh itself.
+__device__ __forceinline__ float2 cap_tanh2(const CapArgs& a, float2 s) {
+  constexpr float c[CAP_TERMS] = {CAP_C[0], CAP_C[1], CAP_C[2], CAP_C[3], CAP_C[4], CAP_C[5], CAP_C[6]};
+  const float2 u = __fmul2_rn(s, make_float2(a.c1, a.c1));
+  const float2 w = __fmul2_rn(u, u);
+  float2 t = make_float2(c[CAP_TERMS - 1], c[CAP_TERMS - 1]);
+#pragma unroll
+  for (int i = CAP_TERMS - 2; i >= 0; --i) t = __ffma2_rn(t, w, make_float2(c[i], c[i]));
+  return __fmul2_rn(u, t);
 }
 
 }  // namespace fa

@@ -241,12 +241,7 @@ __device__ __forceinline__ void probs(const uint32_t (&sr)[32], const float* lse
       if (BIG) {
         th = make_float2(cap_tanh(cap, s.x), cap_tanh(cap, s.y));
       } else {
-        const float2 w = __fmul2_rn(s, s);
-        th = make_float2(cap.tpoly[CAP_TERMS - 1], cap.tpoly[CAP_TERMS - 1]);
-#pragma unroll
-        for (int i = CAP_TERMS - 2; i >= 0; --i)
-          th = __ffma2_rn(th, w, make_float2(cap.tpoly[i], cap.tpoly[i]));
-        th = __fmul2_rn(th, s);
+        th = cap_tanh2(cap, s);
       }
       x = __ffma2_rn(th, make_float2(cap.amp, cap.amp), add);
       g = __ffma2_rn(__fmul2_rn(th, th), make_float2(-UP, -UP), g);
