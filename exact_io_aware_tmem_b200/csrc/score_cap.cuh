@@ -14,14 +14,17 @@ namespace fa {
 // of 50 that moves a logit by 1e-6. tanh.approx (2^-11 relative) would move
 // one of 20 by 0.01, a relative error of P five times its rounding to bf16.
 constexpr int CAP_TERMS = 7;
-constexpr double CAP_C[CAP_TERMS] = {0.9999997019767761,   -0.3333212733268738,
-                                     0.13319575786590576,  -0.05326556786894798,
-                                     0.019972829148173332, -0.005950915161520243,
-                                     0.0009636600152589381};
+__host__ __device__ constexpr float cap_c(int i) {
+  constexpr float c[CAP_TERMS] = {0.9999997019767761f,   -0.3333212733268738f,
+                                  0.13319575786590576f,  -0.05326556786894798f,
+                                  0.019972829148173332f, -0.005950915161520243f,
+                                  0.0009636600152589381f};
+  return c[i];
+}
 
 // By value to the kernels.
 struct CapArgs {
-  float poly[CAP_TERMS];    // A C[i]
+  float poly[CAP_TERMS];    // A cap_c(i)
   float c1;                 // scale / cap: u = c1 s
   float limit;              // 1 / c1: the polynomial holds for |s| <= limit
   float amp;                // A
@@ -35,7 +38,7 @@ inline CapArgs cap_args(float cap, float scale) {
   a.c1 = static_cast<float>(c1);
   a.k2 = static_cast<float>(2.0 * log2e * c1);
   a.limit = static_cast<float>(1.0 / c1);
-  for (int i = 0; i < CAP_TERMS; ++i) a.poly[i] = static_cast<float>(cap * log2e * CAP_C[i]);
+  for (int i = 0; i < CAP_TERMS; ++i) a.poly[i] = static_cast<float>(cap * log2e * cap_c(i));
   return a;
 }
 
@@ -68,12 +71,11 @@ __device__ __forceinline__ float2 cap_poly2(const CapArgs& a, float2 s, float2 a
 
 // The same without A and add: tanh itself.
 __device__ __forceinline__ float2 cap_tanh2(const CapArgs& a, float2 s) {
-  constexpr float c[CAP_TERMS] = {CAP_C[0], CAP_C[1], CAP_C[2], CAP_C[3], CAP_C[4], CAP_C[5], CAP_C[6]};
-  const float2 u = __fmul2_rn(s, make_float2(a.c1, a.c1));
+    const float2 u = __fmul2_rn(s, make_float2(a.c1, a.c1));
   const float2 w = __fmul2_rn(u, u);
-  float2 t = make_float2(c[CAP_TERMS - 1], c[CAP_TERMS - 1]);
+  float2 t = make_float2(cap_c(CAP_TERMS - 1), cap_c(CAP_TERMS - 1));
 #pragma unroll
-  for (int i = CAP_TERMS - 2; i >= 0; --i) t = __ffma2_rn(t, w, make_float2(c[i], c[i]));
+  for (int i = CAP_TERMS - 2; i >= 0; --i) t = __ffma2_rn(t, w, make_float2(cap_c(i), cap_c(i)));
   return __fmul2_rn(u, t);
 }
 

@@ -45,9 +45,10 @@ namespace sfwd {
 
 constexpr int BM = 128;
 constexpr int BN = 128;
-constexpr int THREADS = 320;
-constexpr int WARP_TMA = 8;
-constexpr int WARP_MMA = 9;
+constexpr int SOFTMAX_WARPS = 16;  // two query tiles x two halves of 64 keys x four lane quarters
+constexpr int THREADS = 32 * SOFTMAX_WARPS + 64;
+constexpr int WARP_TMA = 16;
+constexpr int WARP_MMA = 17;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;
 constexpr uint32_t TM_O = 256;
@@ -71,7 +72,8 @@ struct Cfg {
   // p_ready[2], o_full
   static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;   // tmem slot, abort, lo[2], hi[2]
-  static constexpr uint32_t SMEM = OFF_MISC + 32;
+  static constexpr uint32_t OFF_ROW = OFF_MISC + 32;   // float [2 halves][2 BM]: row maxima, sums
+  static constexpr uint32_t SMEM = OFF_ROW + 2 * 2 * BM * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -100,11 +102,32 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const D
   return __all_sync(FULL, ok);
 }
 
+// The two warps that hold the halves of the same 32 rows meet; true for both when
+// both are on track, so that a wait that ran out ends the loops of both at the same
+// barrier.
+__device__ __forceinline__ bool rows_sync(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.and.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
+// TMEM column of k-step kk of P: each 64-key half lies in the first 32 of its own
+// 64 score columns.
+__device__ __forceinline__ uint32_t packed_col(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
+
 __device__ __forceinline__ float pair_max(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// What a row's thread knows of one tile.
+// What a thread knows of its row and its 64 keys of one tile.
+constexpr int HK = 64;
 struct RowTile {
-  int lo, hi;   // visible columns [lo, hi) of the tile
+  int lo, hi;   // visible columns [lo, hi) of the half
   int dist0;    // first key - query
 };
 
@@ -115,7 +138,7 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, const RowTile& t, floa
                                           const CapArgs& cap, float slope2, bool steep, bool& big) {
   float mx[2] = {-INFINITY, -INFINITY}, ab[2] = {0.f, 0.f};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < HK / 32; ++c) {
     uint32_t r[32];
     tmem_ld32(s_col + 32 * c, r);
     tmem_ld_wait();
@@ -150,11 +173,12 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, const RowTile& t, floa
   float x = CAP ? cap_exact(cap, m) : m * c2;
   if (CAP && m == -INFINITY) x = -INFINITY;
   // The key nearest to the query: distance 0, or that of the tile's nearer end.
-  if (BIAS) x -= slope2 * static_cast<float>(max(0, max(t.dist0, -(t.dist0 + BN - 1))));
+  if (BIAS) x -= slope2 * static_cast<float>(max(0, max(t.dist0, -(t.dist0 + HK - 1))));
   return x;
 }
 
-// Second reading: P = 2^(z - m) as bf16 over the first 64 columns of S; returns the row's sum.
+// Second reading: P = 2^(z - m) as bf16 over the first 32 columns of the half; returns the
+// half row's sum.
 template <bool CAP, bool BIAS, bool PARTIAL, bool BIG>
 __device__ __forceinline__ float tile_exp(uint32_t s_col, const RowTile& t, float c2,
                                           const CapArgs& cap, float slope2, float m) {
@@ -162,7 +186,7 @@ __device__ __forceinline__ float tile_exp(uint32_t s_col, const RowTile& t, floa
   // Bias along the row: sl (column) + off, sl of either sign. Where a chunk
   // holds the diagonal the distance is taken per element.
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < HK / 32; ++c) {
     uint32_t r[32];
     tmem_ld32(s_col + 32 * c, r);
     tmem_ld_wait();
@@ -202,7 +226,7 @@ __device__ __forceinline__ float tile_exp(uint32_t s_col, const RowTile& t, floa
       sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], make_float2(p0, p1));
       pk[i >> 1] = pack_bf16x2(p0, p1);
     }
-    // Columns 16 c .. 16 c + 15: scores of chunk c / 2, read already.
+    // Columns 16 c .. 16 c + 15: scores of chunk 0, read already.
     tmem_st16(s_col + 16 * c, pk);
   }
   return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
@@ -241,10 +265,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
-  // This thread's row (softmax warps) and its keys.
-  const int qpos = (m2 * 2 + (warp >> 2)) * BM + (warp & 3) * 32 + lane;
+  // This thread's row (softmax warps) and its keys: warps 0-7 query tile 0, 8-15
+  // tile 1; of each the first four the keys [0, 64) of a tile, the others the rest.
+  const int qpos = (m2 * 2 + (warp >> 3)) * BM + (warp & 3) * 32 + lane;
   KeyRange kr = {0, 0};
-  if (warp < 8 && qpos < sq.len) kr = key_range(p, sh, sq, qpos);
+  if (warp < SOFTMAX_WARPS && qpos < sq.len) kr = key_range(p, sh, sq, qpos);
   if (threadIdx.x == 0) {
     *abort = 0;
     s_lo[0] = s_lo[1] = INT_MAX;
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bars.s_full(g), 1);
-      mbar_init(bars.p_ready(g), 128);
+      mbar_init(bars.p_ready(g), 256);
     }
     mbar_init(bars.o_full(), 1);
     fence_mbar_init();
@@ -270,12 +295,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   __syncthreads();
-  if (warp < 8) {
+  if (warp < SOFTMAX_WARPS && (warp & 4) == 0) {
     const int lo = __reduce_min_sync(FULL, kr.lo < kr.hi ? kr.lo : INT_MAX);
     const int hi = __reduce_max_sync(FULL, kr.hi);
     if (lane == 0 && hi > 0) {
-      atomicMin(&s_lo[warp >> 2], lo);
-      atomicMax(&s_hi[warp >> 2], hi);
+      atomicMin(&s_lo[warp >> 3], lo);
+      atomicMax(&s_hi[warp >> 3], hi);
     }
   }
   tc_fence_before();
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int st = it % VS;
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts_if(leader, tmem + TM_O + g * D, tmem + TM_S + g * BN + kk * 8,
+        mma_ts_if(leader, tmem + TM_O + g * D, tmem + TM_S + g * BN + packed_col(kk),
                   sdesc_add(v_desc, st * TILE + kk * 2048), IDESC_PV,
                   (!fresh || kk > 0) ? 1u : 0u);
     };
@@ -433,59 +458,69 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (n_kv > 0) tc_commit_if(leader, bars.o_full());   // some softmax group waits for it
   } else {
     // ------------------------------------------------------------- softmax ---
-    const int g = warp >> 2;
+    const int g = warp >> 3;            // query tile
+    const int hf = (warp >> 2) & 1;     // half of a tile's keys; half of O's columns
+    const int row = (warp & 3) * 32 + lane;
+    const int bar_id = 1 + g * 4 + (warp & 3);
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + TM_S + g * BN;
-    const uint32_t o_col = tmem + lane_off + TM_O + g * D;
+    const uint32_t s_col = tmem + lane_off + TM_S + g * BN + hf * HK;
+    const uint32_t o_col = tmem + lane_off + TM_O + g * D + hf * (D / 2);
+    float* s_row = reinterpret_cast<float*>(smem + C::OFF_ROW) + g * BM + row;
     const int bg = g ? b_1 : b_0, n = (g ? f_1 : f_0) - bg;
     const float c2 = p.scale_log2;
     const float slope2 = BIAS ? __ldg(sh.slopes + h) * LOG2E : 0.f;
     const bool steep = BIAS && fabsf(slope2) * 127.f > BOUND_LOG2;
     float m_ref = -INFINITY;
-    float l = 0.f;
+    float l = 0.f;    // this half's part of the row's sum
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      const int key0 = (t0 + bg + i) * BN;
+      const int key0 = (t0 + bg + i) * BN + hf * HK;
       RowTile t;
       t.lo = kr.lo - key0;
       t.hi = kr.hi - key0;
       t.dist0 = key0 - qpos;
-      // A warp that sees the whole tile on one side of the diagonal needs no
+      // A warp that sees all 64 keys on one side of the diagonal needs no
       // element-wise mask or distance.
-      const bool whole = __all_sync(FULL, t.lo <= 0 && t.hi >= BN &&
-                                              (!BIAS || t.dist0 >= 0 || t.dist0 + BN <= 1));
-      const bool none = !whole && !__any_sync(FULL, t.lo < BN && t.hi > 0 && t.lo < t.hi);
-      if (!(ok = warp_wait(bars.s_full(g), i & 1, p.err, abort, W_SFULL))) break;
+      const bool whole = __all_sync(FULL, t.lo <= 0 && t.hi >= HK &&
+                                              (!BIAS || t.dist0 >= 0 || t.dist0 + HK <= 1));
+      const bool none = !whole && !__any_sync(FULL, t.lo < HK && t.hi > 0 && t.lo < t.hi);
+      ok = warp_wait(bars.s_full(g), i & 1, p.err, abort, W_SFULL);
       tc_fence_after();
+      bool big = false;
+      float m_cand = -INFINITY;
+      if (ok && !none)
+        m_cand = whole ? tile_max<CAP, BIAS, false>(s_col, t, c2, cap, slope2, steep, big)
+                       : tile_max<CAP, BIAS, true>(s_col, t, c2, cap, slope2, steep, big);
+      // The other half's maximum. One slot is enough: the partner writes its next
+      // one after S of the next step, which follows P of this step from both.
+      s_row[hf * 2 * BM] = m_cand;
+      if (!(ok = rows_sync(bar_id, ok))) break;
+      const float other = s_row[(hf ^ 1) * 2 * BM];
+      m_cand = fmaxf(m_cand, other);
+      const bool grow = m_cand > m_ref + RESCALE_LOG2;   // always true on the first visible tile
+      const float m_new = grow ? m_cand : m_ref;
+      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
       float alpha = 1.f;
+      if (grow && m_ref != -INFINITY) alpha = ex2_approx(m_ref - m_use);
+      m_ref = m_new;
+      float sum = 0.f;
       if (none) {
         const uint32_t z[16] = {};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(s_col + 16 * c, z);
+        tmem_st16(s_col, z);
+        tmem_st16(s_col + 16, z);
+      } else if (CAP && big) {
+        sum = whole ? tile_exp<CAP, BIAS, false, CAP>(s_col, t, c2, cap, slope2, m_use)
+                    : tile_exp<CAP, BIAS, true, CAP>(s_col, t, c2, cap, slope2, m_use);
       } else {
-        bool big = false;
-        const float m_cand =
-            whole ? tile_max<CAP, BIAS, false>(s_col, t, c2, cap, slope2, steep, big)
-                  : tile_max<CAP, BIAS, true>(s_col, t, c2, cap, slope2, steep, big);
-        const bool grow = m_cand > m_ref + RESCALE_LOG2;   // always true on the first visible tile
-        const float m_new = grow ? m_cand : m_ref;
-        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-        float sum;
-        if (CAP && big)
-          sum = whole ? tile_exp<CAP, BIAS, false, CAP>(s_col, t, c2, cap, slope2, m_use)
-                      : tile_exp<CAP, BIAS, true, CAP>(s_col, t, c2, cap, slope2, m_use);
-        else
-          sum = whole ? tile_exp<CAP, BIAS, false, false>(s_col, t, c2, cap, slope2, m_use)
-                      : tile_exp<CAP, BIAS, true, false>(s_col, t, c2, cap, slope2, m_use);
-        if (grow && m_ref != -INFINITY) alpha = ex2_approx(m_ref - m_use);
-        l = l * alpha + sum;
-        m_ref = m_new;
+        sum = whole ? tile_exp<CAP, BIAS, false, false>(s_col, t, c2, cap, slope2, m_use)
+                    : tile_exp<CAP, BIAS, true, false>(s_col, t, c2, cap, slope2, m_use);
       }
+      l = l * alpha + sum;
       // The reference moved: O, which holds the earlier tiles only (S_g of this
       // step completing means P_g V of the previous one has), moves with it.
       if (i > 0 && __any_sync(FULL, alpha != 1.f)) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t o[32];
           tmem_ld32(o_col + 32 * c, o);
           tmem_ld_wait();
@@ -502,13 +537,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ epilogue ---
     const bool row_ok = qpos < sq.len;
     const size_t out_row = static_cast<size_t>(sq.start + qpos) * p.H + h;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D + hf * (D / 2));
     if (n > 0) ok = ok && warp_wait(bars.o_full(), 0, p.err, abort, W_OFULL);
+    s_row[hf * 2 * BM] = l;   // o_full: the partner has read the last maximum
+    ok = rows_sync(bar_id, ok);
+    l += s_row[(hf ^ 1) * 2 * BM];
     if (ok) {
       tc_fence_after();
       const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld32(o_col + 32 * c, o);
@@ -530,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (row_ok)
+      if (row_ok && hf == 0)
         p.lse[lse_index(p, b, h, sq.start, qpos)] =
             (l > 0.f) ? (m_ref + __log2f(l)) * LN2 : -INFINITY;
     }
