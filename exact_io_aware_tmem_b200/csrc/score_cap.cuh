@@ -22,8 +22,16 @@ __host__ __device__ constexpr float cap_c(int i) {
   return c[i];
 }
 
+// The same over |u| <= 0.6 with five coefficients: 2.0e-8 too.
+constexpr int CAP_FEW = 5;
+constexpr double CAP_FEW_C[CAP_FEW] = {0.9999996423721313, -0.33331209421157837, 0.13299210369586945,
+                                       -0.051696743816137314, 0.01497695967555046};
+constexpr double CAP_FEW_END = 0.6;
+
 // By value to the kernels.
 struct CapArgs {
+  float few[CAP_FEW];       // A c1^(2 i + 1) CAP_FEW_C[i], on s itself: one product less
+  float few_limit;          // 0.6 / c1, or -1 where a power of c1 leaves fp32's normal range
   float poly[CAP_TERMS];    // A cap_c(i)
   float c1;                 // scale / cap: u = c1 s
   float limit;              // 1 / c1: the polynomial holds for |s| <= limit
@@ -38,6 +46,12 @@ inline CapArgs cap_args(float cap, float scale) {
   a.c1 = static_cast<float>(c1);
   a.k2 = static_cast<float>(2.0 * log2e * c1);
   a.limit = static_cast<float>(1.0 / c1);
+  a.few_limit = static_cast<float>(CAP_FEW_END / c1);
+  double pw = cap * log2e * c1;
+  for (int i = 0; i < CAP_FEW; ++i, pw *= c1 * c1) {
+    a.few[i] = static_cast<float>(pw * CAP_FEW_C[i]);
+    if (!isfinite(a.few[i]) || fabs(a.few[i]) < 1e-37) a.few_limit = -1.f;
+  }
   for (int i = 0; i < CAP_TERMS; ++i) a.poly[i] = static_cast<float>(cap * log2e * cap_c(i));
   return a;
 }
@@ -67,6 +81,15 @@ __device__ __forceinline__ float2 cap_poly2(const CapArgs& a, float2 s, float2 a
   for (int i = CAP_TERMS - 2; i >= 0; --i)
     t = __ffma2_rn(t, w, make_float2(a.poly[i], a.poly[i]));
   return __ffma2_rn(u, t, add);
+}
+
+// The same for |s| <= few_limit.
+__device__ __forceinline__ float2 cap_few2(const CapArgs& a, float2 s, float2 add) {
+  const float2 w = __fmul2_rn(s, s);
+  float2 t = make_float2(a.few[CAP_FEW - 1], a.few[CAP_FEW - 1]);
+#pragma unroll
+  for (int i = CAP_FEW - 2; i >= 0; --i) t = __ffma2_rn(t, w, make_float2(a.few[i], a.few[i]));
+  return __ffma2_rn(s, t, add);
 }
 
 // The same without A and add: tanh itself.

@@ -232,13 +232,90 @@ __device__ __forceinline__ float tile_exp(uint32_t s_col, const RowTile& t, floa
   return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
 }
 
-template <int D, bool CAP, bool BIAS>
+// Under a cap and without a bias the scores lie in [-A, A], and while A <= 90 no
+// maximum is needed: with the reference m = ceil(A) - 80, P = 2^(x - m) lies in
+// [2^-101, 2^80] whatever the row holds; bf16 and fp32 keep their relative precision
+// over that range, and the sums stay below 2^127 for 2^31 keys of |v| up to 2^16. The
+// scores are then read once, no half waits for the other's maximum and O is never
+// rescaled. Per 32 scores the cheapest form of the cap that their largest allows.
+constexpr float FIXED_AMP = 90.f;
+constexpr float FIXED_TOP = 80.f;
+
+template <bool PARTIAL, int FORM>
+__device__ __forceinline__ void fixed_chunk(const uint32_t (&r)[32], int lo, int hi,
+                                            const CapArgs& cap, float m, float2 (&sum)[2],
+                                            uint32_t (&pk)[16]) {
+  const float2 add = make_float2(-m, -m);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 s = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+    float2 x;
+    if (FORM == 0)
+      x = cap_few2(cap, s, add);
+    else if (FORM == 1)
+      x = cap_poly2(cap, s, add);
+    else
+      x = make_float2(fmaf(cap.amp, cap_tanh(cap, s.x), -m), fmaf(cap.amp, cap_tanh(cap, s.y), -m));
+    float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+    if (PARTIAL) {
+      p0 = (i >= lo && i < hi) ? p0 : 0.f;
+      p1 = (i + 1 >= lo && i + 1 < hi) ? p1 : 0.f;
+    }
+    sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], make_float2(p0, p1));
+    pk[i >> 1] = pack_bf16x2(p0, p1);
+  }
+}
+
+template <bool PARTIAL>
+__device__ __forceinline__ float tile_fixed(uint32_t s_col, const RowTile& t, const CapArgs& cap,
+                                            float m) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < HK / 32; ++c) {
+    uint32_t r[32], pk[16];
+    tmem_ld32(s_col + 32 * c, r);
+    tmem_ld_wait();
+    reg_fence(r);
+    float ab[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      ab[(i >> 1) & 1] = pair_max(ab[(i >> 1) & 1], fabsf(__uint_as_float(r[i])),
+                                  fabsf(__uint_as_float(r[i + 1])));
+    const float most = fmaxf(ab[0], ab[1]);
+    const int lo = t.lo - 32 * c, hi = t.hi - 32 * c;
+    if (!__any_sync(FULL, most > cap.few_limit))
+      fixed_chunk<PARTIAL, 0>(r, lo, hi, cap, m, sum, pk);
+    else if (!__any_sync(FULL, most > cap.limit))
+      fixed_chunk<PARTIAL, 1>(r, lo, hi, cap, m, sum, pk);
+    else
+      fixed_chunk<PARTIAL, 2>(r, lo, hi, cap, m, sum, pk);
+    tmem_st16(s_col + 16 * c, pk);
+  }
+  return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+}
+
+// (m + log2 l) ln 2, the exponent of l apart: under the fixed reference it is a large
+// part of log2 l, whose approximation has a relative error.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  if (!(l > 0.f)) return -INFINITY;
+  const int e = (__float_as_int(l) >> 23) - 127;
+  const float f = __int_as_float((__float_as_int(l) & 0x007fffff) | 0x3f800000);
+  return (m + static_cast<float>(e) + __log2f(f)) * LN2;
+}
+
+// MODE: which parts of the shape the scores have (key ranges always).
+enum Mode : int { RANGES = 0, BIASED = 1, CAPPED = 2, CAPPED_BIASED = 3, CAPPED_FIXED = 4 };
+
+template <int D, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     shaped_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const AttnParams p,
                       const ShapeArgs sh, const CapArgs cap, int num_m2, int group) {
   using C = Cfg<D>;
+  constexpr bool BIAS = MODE == BIASED || MODE == CAPPED_BIASED;
+  constexpr bool CAP = MODE >= CAPPED;
+  constexpr bool FIXED = MODE == CAPPED_FIXED;
   constexpr int KS = C::KS, VS = C::VS;
   constexpr uint32_t TILE = C::TILE, OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -470,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float c2 = p.scale_log2;
     const float slope2 = BIAS ? __ldg(sh.slopes + h) * LOG2E : 0.f;
     const bool steep = BIAS && fabsf(slope2) * 127.f > BOUND_LOG2;
-    float m_ref = -INFINITY;
+    float m_ref = FIXED ? ceilf(cap.amp) - FIXED_TOP : -INFINITY;
     float l = 0.f;    // this half's part of the row's sum
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
@@ -486,48 +563,59 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool none = !whole && !__any_sync(FULL, t.lo < HK && t.hi > 0 && t.lo < t.hi);
       ok = warp_wait(bars.s_full(g), i & 1, p.err, abort, W_SFULL);
       tc_fence_after();
-      bool big = false;
-      float m_cand = -INFINITY;
-      if (ok && !none)
-        m_cand = whole ? tile_max<CAP, BIAS, false>(s_col, t, c2, cap, slope2, steep, big)
-                       : tile_max<CAP, BIAS, true>(s_col, t, c2, cap, slope2, steep, big);
-      // The other half's maximum. One slot is enough: the partner writes its next
-      // one after S of the next step, which follows P of this step from both.
-      s_row[hf * 2 * BM] = m_cand;
-      if (!(ok = rows_sync(bar_id, ok))) break;
-      const float other = s_row[(hf ^ 1) * 2 * BM];
-      m_cand = fmaxf(m_cand, other);
-      const bool grow = m_cand > m_ref + RESCALE_LOG2;   // always true on the first visible tile
-      const float m_new = grow ? m_cand : m_ref;
-      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-      float alpha = 1.f;
-      if (grow && m_ref != -INFINITY) alpha = ex2_approx(m_ref - m_use);
-      m_ref = m_new;
-      float sum = 0.f;
-      if (none) {
-        const uint32_t z[16] = {};
-        tmem_st16(s_col, z);
-        tmem_st16(s_col + 16, z);
-      } else if (CAP && big) {
-        sum = whole ? tile_exp<CAP, BIAS, false, CAP>(s_col, t, c2, cap, slope2, m_use)
-                    : tile_exp<CAP, BIAS, true, CAP>(s_col, t, c2, cap, slope2, m_use);
+      if constexpr (FIXED) {
+        if (!ok) break;
+        if (none) {
+          const uint32_t z[16] = {};
+          tmem_st16(s_col, z);
+          tmem_st16(s_col + 16, z);
+        } else {
+          l += whole ? tile_fixed<false>(s_col, t, cap, m_ref) : tile_fixed<true>(s_col, t, cap, m_ref);
+        }
       } else {
-        sum = whole ? tile_exp<CAP, BIAS, false, false>(s_col, t, c2, cap, slope2, m_use)
-                    : tile_exp<CAP, BIAS, true, false>(s_col, t, c2, cap, slope2, m_use);
-      }
-      l = l * alpha + sum;
-      // The reference moved: O, which holds the earlier tiles only (S_g of this
-      // step completing means P_g V of the previous one has), moves with it.
-      if (i > 0 && __any_sync(FULL, alpha != 1.f)) {
+        bool big = false;
+        float m_cand = -INFINITY;
+        if (ok && !none)
+          m_cand = whole ? tile_max<CAP, BIAS, false>(s_col, t, c2, cap, slope2, steep, big)
+                         : tile_max<CAP, BIAS, true>(s_col, t, c2, cap, slope2, steep, big);
+        // The other half's maximum. One slot is enough: the partner writes its next
+        // one after S of the next step, which follows P of this step from both.
+        s_row[hf * 2 * BM] = m_cand;
+        if (!(ok = rows_sync(bar_id, ok))) break;
+        const float other = s_row[(hf ^ 1) * 2 * BM];
+        m_cand = fmaxf(m_cand, other);
+        const bool grow = m_cand > m_ref + RESCALE_LOG2;   // always true on the first visible tile
+        const float m_new = grow ? m_cand : m_ref;
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        float alpha = 1.f;
+        if (grow && m_ref != -INFINITY) alpha = ex2_approx(m_ref - m_use);
+        m_ref = m_new;
+        float sum = 0.f;
+        if (none) {
+          const uint32_t z[16] = {};
+          tmem_st16(s_col, z);
+          tmem_st16(s_col + 16, z);
+        } else if (CAP && big) {
+          sum = whole ? tile_exp<CAP, BIAS, false, CAP>(s_col, t, c2, cap, slope2, m_use)
+                      : tile_exp<CAP, BIAS, true, CAP>(s_col, t, c2, cap, slope2, m_use);
+        } else {
+          sum = whole ? tile_exp<CAP, BIAS, false, false>(s_col, t, c2, cap, slope2, m_use)
+                      : tile_exp<CAP, BIAS, true, false>(s_col, t, c2, cap, slope2, m_use);
+        }
+        l = l * alpha + sum;
+        // The reference moved: O, which holds the earlier tiles only (S_g of this
+        // step completing means P_g V of the previous one has), moves with it.
+        if (i > 0 && __any_sync(FULL, alpha != 1.f)) {
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_col + 32 * c, o);
-          tmem_ld_wait();
-          reg_fence(o);
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_col + 32 * c, o);
+            tmem_ld_wait();
+            reg_fence(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(o_col + 32 * c, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(o_col + 32 * c, o);
+          }
         }
       }
       tmem_st_wait();
@@ -570,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (row_ok && hf == 0)
         p.lse[lse_index(p, b, h, sq.start, qpos)] =
-            (l > 0.f) ? (m_ref + __log2f(l)) * LN2 : -INFINITY;
+            row_lse(m_ref, l);
     }
   }
 
@@ -582,7 +670,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int MODE>
 cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
   using C = Cfg<D>;
   const int num_m2 = (p.max_seqlen + 2 * BM - 1) / (2 * BM);
@@ -593,21 +681,23 @@ cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream
       !make_tmap_bf16_2d(&tk, p.k, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN) ||
       !make_tmap_bf16_2d(&tv, p.v, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(shaped_fwd_kernel<D, CAP, BIAS>,
+  const cudaError_t e = cudaFuncSetAttribute(shaped_fwd_kernel<D, MODE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int group = l2_group(4ll * p.max_seqlen * D, p.H / p.H_kv, p.H * p.B);
-  const CapArgs cap = CAP ? cap_args(sh.cap, p.scale) : CapArgs{};
-  shaped_fwd_kernel<D, CAP, BIAS><<<static_cast<unsigned>(tiles), THREADS, C::SMEM, stream>>>(
+  const CapArgs cap = MODE >= CAPPED ? cap_args(sh.cap, p.scale) : CapArgs{};
+  shaped_fwd_kernel<D, MODE><<<static_cast<unsigned>(tiles), THREADS, C::SMEM, stream>>>(
       tq, tk, tv, p, sh, cap, num_m2, group);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
-  const bool cap = sh.cap > 0.f, bias = sh.slopes != nullptr;
-  if (cap) return bias ? launch<D, true, true>(p, sh, stream) : launch<D, true, false>(p, sh, stream);
-  return bias ? launch<D, false, true>(p, sh, stream) : launch<D, false, false>(p, sh, stream);
+  const bool bias = sh.slopes != nullptr;
+  if (!(sh.cap > 0.f)) return bias ? launch<D, BIASED>(p, sh, stream) : launch<D, RANGES>(p, sh, stream);
+  if (bias) return launch<D, CAPPED_BIASED>(p, sh, stream);
+  return sh.cap * LOG2E <= FIXED_AMP ? launch<D, CAPPED_FIXED>(p, sh, stream)
+                                     : launch<D, CAPPED>(p, sh, stream);
 }
 
 }  // namespace sfwd

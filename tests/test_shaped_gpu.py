@@ -180,6 +180,33 @@ def test_cap_far_into_saturation(D, std, scale):
              scale=scale)
 
 
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 62.0, 70.0, 300.0, 1e5])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_of_every_size(D, cap):
+    # Below and above the size up to which the forward needs no running maximum; logits of
+    # std 4 and, at a scale of 2, far over 100.
+    run_case(11, "bf16", [300], 2, 1, D, False, True, cap, False, "none", std=2.0)
+    run_case(12, "bf16", [300], 2, 1, D, False, False, cap, False, "any", std=2.0, scale=2.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_rows_all_at_one_end_of_the_cap(D, sign):
+    # Every score of a row saturates at the same end: P sits at an end of its range.
+    n, H, cap = 260, 2, 60.0
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((n, H, D), generator=g).abs() * 8
+    k = sign * torch.randn((n, H, D), generator=g).abs() * 8
+    v = torch.randn((n, H, D), generator=g)
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    o, lse = fa.fwd(*(x.cuda()[None] for x in (q, k, v)), causal=True, softcap=cap, scale=1.0)
+    clean()
+    r = osh.forward(q, k, v, [0, n], True, 1.0, cap)
+    e = score_error(q, k, 1.0, cap, None, n, "bf16")
+    inside("LSE", f64(lse)[0], r.lse, e)
+    inside("O", f64(o)[0], r.o, (HALF + 2 * e) * r.o_abs + HALF * np.abs(r.o))
+
+
 def test_ranges_that_see_nothing():
     q = torch.randn(2, 200, 4, 64, device="cuda", dtype=torch.bfloat16)
     z = torch.zeros(2, 200, dtype=torch.int32, device="cuda")
