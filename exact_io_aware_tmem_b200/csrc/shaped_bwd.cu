@@ -25,8 +25,8 @@
 // - The factor of dP - D. P (1 - t^2) 2^14 waits as fp16 for dP: 11 bits down to
 //   P = 4e-9, where bf16 would add a rounding of 2^-9 to that of dX. The 2^14
 //   leaves again with the scale of dQ and dK.
-// - The cap by its polynomial per 32 scores, or by exponential and reciprocal
-//   where one is out of its range (score_cap.cuh).
+// - The cap per 32 scores by the shortest polynomial that their largest allows, or by
+//   exponential and reciprocal (score_cap.cuh).
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>
@@ -207,7 +207,7 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t v) {
 // 32 scores of a key row (queries q0 .. q0 + 31 of the step): P as packed bf16
 // and F = P (1 - t^2) 2^14 as packed fp16. d0 = first query - key; lse holds
 // -LSE log2 e.
-template <bool CAP, bool BIAS, bool BIG>
+template <bool CAP, bool BIAS, int FORM>
 __device__ __forceinline__ void probs(const uint32_t (&sr)[32], const float* lse, float c2,
                                       const CapArgs& cap, float slope2, int d0,
                                       uint32_t (&pk)[16], uint32_t* f) {
@@ -236,13 +236,13 @@ __device__ __forceinline__ void probs(const uint32_t (&sr)[32], const float* lse
     float2 x, g = make_float2(UP, UP);
     if (!CAP) {
       x = __ffma2_rn(s, make_float2(c2, c2), add);
+    } else if (FORM < 2) {
+      const float2 y = __fmul2_rn(s, cap_poly2<FORM>(cap, s));   // A t
+      const float k = -UP * cap.inv_amp2;
+      x = __fadd2_rn(y, add);
+      g = __ffma2_rn(__fmul2_rn(y, y), make_float2(k, k), g);
     } else {
-      float2 th;
-      if (BIG) {
-        th = make_float2(cap_tanh(cap, s.x), cap_tanh(cap, s.y));
-      } else {
-        th = cap_tanh2(cap, s);
-      }
+      const float2 th = make_float2(cap_tanh(cap, s.x), cap_tanh(cap, s.y));
       x = __ffma2_rn(th, make_float2(cap.amp, cap.amp), add);
       g = __ffma2_rn(__fmul2_rn(th, th), make_float2(-UP, -UP), g);
     }
@@ -652,20 +652,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld32(tmem + lane_off + C::TM_S + 64 * hf + 32 * c, sr);
         tmem_ld_wait();
         reg_fence(sr);
-        bool big = false;
+        int form = 0;
         if (CAP) {
           float ab[2] = {0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < 32; q += 2)
             ab[(q >> 1) & 1] = fmaxf(fmaxf(ab[(q >> 1) & 1], fabsf(__uint_as_float(sr[q]))),
                                      fabsf(__uint_as_float(sr[q + 1])));
-          big = __any_sync(FULL, fmaxf(ab[0], ab[1]) > cap.limit);
+          form = cap_form(cap, fmaxf(ab[0], ab[1]));
         }
         const int d0 = qbase + 32 * c - kpos;
-        if (CAP && big)
-          probs<CAP, BIAS, CAP>(sr, lse_t + 32 * c, c2, cap, slope2, d0, pk, f + 16 * c);
+        if (!CAP || form == 0)
+          probs<CAP, BIAS, 0>(sr, lse_t + 32 * c, c2, cap, slope2, d0, pk, f + 16 * c);
+        else if (form == 1)
+          probs<CAP, BIAS, 1>(sr, lse_t + 32 * c, c2, cap, slope2, d0, pk, f + 16 * c);
         else
-          probs<CAP, BIAS, false>(sr, lse_t + 32 * c, c2, cap, slope2, d0, pk, f + 16 * c);
+          probs<CAP, BIAS, 2>(sr, lse_t + 32 * c, c2, cap, slope2, d0, pk, f + 16 * c);
         if (!full) mask_words(vis_t + 32 * c, r, pk, f + 16 * c);
         // P^T over the first 32 of this half's own 64 S^T columns.
         tmem_st16(tmem + lane_off + C::TM_S + 64 * hf + 16 * c, pk);

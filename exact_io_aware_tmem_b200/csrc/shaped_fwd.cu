@@ -17,8 +17,8 @@
 // of a tile's 128 keys, TMEM lane quarter), warp 16 TMA, warp 17 MMA. S_g at TMEM
 // columns [128 g, 128 g + 128), P_g as bf16 over the first 32 columns of either half
 // of S_g, O_g from 256 on; per step P_0 V, S_0 of the next, P_1 V, S_1 of the next.
-// Sixteen warps instead of eight: the cap costs six fused multiply-adds on packed
-// pairs a score pair and the exponential one of 16 lanes a clock, and four warps a
+// Sixteen warps instead of eight: the cap costs five products on packed pairs a score
+// pair and the exponential one of 16 lanes a clock, and four warps a
 // scheduler keep both busy.
 //
 // One reading of S. The reference a tile's P are taken at is the maximum of the tiles
@@ -28,8 +28,8 @@
 // reference 0, is the tile read again for its maximum first; the two warps of the
 // same rows agree on that with one barrier.
 //
-// The cap. Up to |s| <= 0.6 cap / scale a polynomial of five terms, up to cap / scale
-// one of seven (score_cap.cuh), which leave the special-function unit to the one
+// The cap. Up to |s| <= 0.4 cap / scale a polynomial of four terms, up to 0.8 cap /
+// scale one of six (score_cap.cuh), which leave the special-function unit to the one
 // exponential a score; a warp with a larger score among 16 columns takes tanh by
 // exponential and reciprocal there.
 //
@@ -207,10 +207,8 @@ __device__ __forceinline__ void chunk(const uint32_t (&r)[16], int lo, int hi, i
     float2 x;
     if (!has_cap(MODE))
       x = __ffma2_rn(s, make_float2(c2, c2), add);
-    else if (FORM == 0)
-      x = cap_few2(cap, s, add);
-    else if (FORM == 1)
-      x = cap_poly2(cap, s, add);
+    else if (FORM < 2)
+      x = __ffma2_rn(s, cap_poly2<FORM>(cap, s), add);
     else
       x = make_float2(fmaf(cap.amp, cap_tanh(cap, s.x), add.x), fmaf(cap.amp, cap_tanh(cap, s.y), add.y));
     if (PARTIAL) {
@@ -256,10 +254,10 @@ __device__ __forceinline__ float half_tile(uint32_t s_col, const RowTile& t, flo
       for (int i = 0; i < 16; i += 2)
         ab[(i >> 1) & 1] = max3(ab[(i >> 1) & 1], fabsf(__uint_as_float(q[i])),
                                 fabsf(__uint_as_float(q[i + 1])));
-      const float most = fmaxf(ab[0], ab[1]);
-      if (!__any_sync(FULL, most > cap.few_limit))
+      const int form = cap_form(cap, fmaxf(ab[0], ab[1]));
+      if (form == 0)
         chunk<MODE, PARTIAL, EXP, 0>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
-      else if (!__any_sync(FULL, most > cap.limit))
+      else if (form == 1)
         chunk<MODE, PARTIAL, EXP, 1>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
       else
         chunk<MODE, PARTIAL, EXP, 2>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
