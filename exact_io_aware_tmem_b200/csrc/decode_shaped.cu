@@ -11,7 +11,9 @@
 // What the shape adds. A thread owns one key and NQ / 2 of the rows, so the cap
 // (tanh by exponential and reciprocal), the bias (slope x distance of two
 // positions) and the window are a few instructions on a few scores, hidden
-// behind the cache's stream. With a window the units are the tiles from the
+// behind the cache's stream. A segment's tiles are walked from its end: with a bias
+// the newest keys hold the maximum, and the reference of the softmax then hardly
+// moves (each move is two barriers and a pass over O^T). With a window the units are the tiles from the
 // first one a query sees: the others are never read.
 //
 // The weights. A slot's weight needs the row's final LSE, which no CTA has while
@@ -65,7 +67,7 @@ struct Cfg {
   static constexpr uint32_t OFF_ALPHA = OFF_MREF + NQ * 4;    // float [NQ]: its last move
   static constexpr uint32_t OFF_RED = OFF_ALPHA + NQ * 4;     // float [4][NQ]: per-warp max / sum
   static constexpr uint32_t OFF_SLOPE = OFF_RED + 4 * NQ * 4; // float [NQ]: slope log2 e of a row
-  static constexpr uint32_t OFF_QPOS = OFF_SLOPE + NQ * 4;    // int [NQ]: a row's position
+  static constexpr uint32_t OFF_QPOS = OFF_SLOPE + NQ * 4;    // int [NQ]: a row's position - row 0's
   static constexpr uint32_t OFF_ROWS = OFF_QPOS + NQ * 4;  // int [8][8]: paged rows per tile
   static constexpr uint32_t OFF_BAR = OFF_ROWS + 8 * 8 * 4;
   // k_full[S], k_empty[S], v_full[S], v_empty[S], q_full[QBUF], q_empty[QBUF],
@@ -249,17 +251,17 @@ __device__ __forceinline__ int seq_tiles(const Lens& s, int b, int& first, int& 
 // sequence b, unit u. Every role walks the same sequence of tiles.
 struct Walk {
   int b, t;
-  int f, n, len;            // tiles [f, n) and keys of sequence b
+  int f, n, len;            // tiles [f, n) and keys of sequence b, walked from the last
   long long u, u0, u1;      // current unit, the CTA's range [u0, u1)
   __device__ bool done() const { return u >= u1; }
   // First / last tile of its piece (the part of a segment inside the range).
-  __device__ bool first() const { return t == f || u == u0; }
-  __device__ bool last() const { return t + 1 == n || u + 1 == u1; }
-  __device__ bool seg_end() const { return t + 1 == n; }
+  __device__ bool first() const { return t + 1 == n || u == u0; }
+  __device__ bool last() const { return t == f || u + 1 == u1; }
+  __device__ bool tail() const { return t + 1 == n; }
   __device__ void next(const Lens& s) {
     ++u;
-    ++t;
-    if (u >= u1 || t < n) return;
+    --t;
+    if (u >= u1 || t >= f) return;
     do {
       if (++b >= s.B) {
         u = u1;
@@ -267,13 +269,13 @@ struct Walk {
       }
       n = seq_tiles(s, b, f, len);
     } while (n == 0);
-    t = f;
+    t = n - 1;
   }
   // To the first tile of the next piece.
   __device__ void next_piece(const Lens& s) {
-    const long long step = (n - t < u1 - u) ? static_cast<long long>(n - t) : u1 - u;
+    const long long step = (t - f + 1 < u1 - u) ? static_cast<long long>(t - f + 1) : u1 - u;
     u += step - 1;
-    t += static_cast<int>(step - 1);
+    t -= static_cast<int>(step - 1);
     next(s);
   }
 };
@@ -347,9 +349,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) tot += __shfl_xor_sync(FULL, tot, sh);
-    const long long u0 = tot * grp / groups;
-    const long long u1 = tot * (grp + 1) / groups;
-    int sb = 0, sf = 0;
+    // No more ranges than units: an empty one inside a segment would be one more
+    // partial for the merge to read.
+    const long long used = min(tot, static_cast<long long>(groups));
+    const long long u0 = grp < used ? tot * grp / used : tot;
+    const long long u1 = grp < used ? tot * (grp + 1) / used : tot;
+    int sb = 0, sl = 0;
     long long base = 0;
     if (u0 < tot) {
       long long acc = 0;
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int src = __ffs(hit) - 1;
           sb = b0 + src;
           base = __shfl_sync(FULL, excl, src);
-          sf = __shfl_sync(FULL, f, src);
+          sl = __shfl_sync(FULL, n, src) - 1;
           break;
         }
         acc = __shfl_sync(FULL, incl, 31);
@@ -380,16 +385,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const long long off = u0 - base;   // < n_sb when u0 < tot
     if (lane == 0) {
       start[0] = sb;
-      start[1] = static_cast<int>(u0 < tot ? sf + off : 0);
+      start[1] = static_cast<int>(u0 < tot ? sl - off : 0);
       range[0] = u0;
       range[1] = u1;
-    }
-    if (u0 == u1 && u0 < tot && off != 0) {
-      // An empty range strictly inside a segment (more groups than tiles):
-      // the segment's pieces lie on both sides, so the merge reads this
-      // CTA's slot too. It holds no key: LSE -inf.
-      const size_t slot = static_cast<size_t>((sb + grp) * p.H_kv + hk) * R;
-      for (int r = lane; r < R; r += 32) dt.lse_part[slot + r] = -INFINITY;
     }
   }
   if (warp == WARP_MMA) {
@@ -408,6 +406,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // finish_kernel may take its places now; it waits for this grid's end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk w0;
   w0.b = start[0];
   w0.t = start[1];
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // lane u box u of a paged tile. Three independent streams: Q per piece
     // (once the buffer's last score MMA is done), K and V per tile; K leads.
     // Paged cache: the K stream reads the page ids of its sequence 32 at a
-    // time (lane L holding page base + L, the next batch in flight), takes a
+    // time (lane L holding page base + L, the batch before it in flight), takes a
     // tile's ids by shuffle and leaves the tile's rows in a ring of 8 for the
     // V stream, which reads the same rows.
     const bool paged = dec.block_table != nullptr;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     auto page_id = [&](const Walk& w, int pg) -> int {
       const int n_pages = (w.len + dec.page - 1) / max(dec.page, 1);
-      return (pg < n_pages && pg < dec.max_blocks)
+      return (pg >= 0 && pg < n_pages && pg < dec.max_blocks)
                  ? __ldg(dec.block_table + static_cast<size_t>(w.b) * dec.max_blocks + pg)
                  : -1;
     };
@@ -450,15 +450,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     PageBatch kpb{0, -1, -1};
     auto tile_row = [&](const Walk& w) -> int {
       const int pg0 = (box < BN) ? w.t * n_box : w.t / tpp;
+      const int base = pg0 & ~31;
       if (w.first()) {
-        kpb.base = pg0;
-        kpb.cur = page_id(w, pg0 + lane);
-        kpb.nxt = page_id(w, pg0 + 32 + lane);
-      }
-      while (pg0 >= kpb.base + 32) {
-        kpb.base += 32;
+        kpb.base = base;
+        kpb.cur = page_id(w, base + lane);
+        kpb.nxt = page_id(w, base - 32 + lane);
+      } else if (base != kpb.base) {
+        kpb.base = base;
         kpb.cur = kpb.nxt;
-        kpb.nxt = page_id(w, kpb.base + 32 + lane);
+        kpb.nxt = page_id(w, base - 32 + lane);
       }
       const int blk = __shfl_sync(FULL, kpb.cur, (pg0 + min(lane, n_box - 1) - kpb.base) & 31);
       int row = static_cast<int>(dec.cache_rows);
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           warp_test(bars.v_empty(jv % STAGES), ((jv / STAGES) & 1) ^ 1)) {
         const int st = jv % STAGES;
         const uint32_t dst = sbase + C::OFF_V + st * TILE;
-        if (!(vw.seg_end() && (vw.len % BN) != 0)) {
+        if (!(vw.tail() && (vw.len % BN) != 0)) {
           if (lane == 0) mbar_arrive_expect_tx(bars.v_full(st), TILE);
           __syncwarp();
           load_kv(dst, &tm_v, bars.v_full(st), vw, jv, false);
@@ -757,6 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int r = 0; r < NH; ++r) l[r] = 0.f;
     int i = 0;     // the CTA's tile counter
     int t0 = 0;    // first tile of the current piece
+    int q0 = 0;    // position of the sequence's first query token
     bool ok = true;
     while (!w.done()) {
       const bool first = w.first();
@@ -768,11 +769,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The rows' positions (a token before slot 0 has its slot number).
         if (sid < NQ) {
           const int slot = w.len - dec.q_len + sid / g;
-          qpos_s[sid] = (placed && sid < R && slot >= 0)
-                            ? __ldg(sh.key_positions +
-                                    (static_cast<size_t>(w.b) * p.H_kv + hk) * sh.slots + slot)
-                            : slot;
+          const int s0 = w.len - dec.q_len;
+          const int* pos = placed ? sh.key_positions +
+                                        (static_cast<size_t>(w.b) * p.H_kv + hk) * sh.slots
+                                  : nullptr;
+          const int here = (placed && sid < R && slot >= 0) ? __ldg(pos + slot) : slot;
+          qpos_s[sid] = here - ((placed && s0 >= 0) ? __ldg(pos + s0) : s0);
         }
+        q0 = w.len - dec.q_len;
+        if (placed && q0 >= 0)
+          q0 = __ldg(sh.key_positions + (static_cast<size_t>(w.b) * p.H_kv + hk) * sh.slots + q0);
         softmax_sync();
       }
       const int key = w.t * BN + kt;
@@ -794,10 +800,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float v = __uint_as_float(s[r]);
         x[r] = capped ? cap_exact(cap, v) : v * c2;
       }
+      const int dist = q0 - kpos;   // of row 0; row r is qpos_s[r] further on
       if (biased) {
+        const float d = static_cast<float>(dist);
 #pragma unroll
         for (int r = 0; r < NH; ++r)
-          x[r] = fmaf(-slope_s[r0 + r], fabsf(static_cast<float>(qpos_s[r0 + r] - kpos)), x[r]);
+          x[r] = fmaf(-slope_s[r0 + r], fabsf(d + static_cast<float>(qpos_s[r0 + r])), x[r]);
       }
       // Query row r sees key `key` when key < len, causally key <= len - q_len +
       // r / g, i.e. r >= g (key - len + q_len), and within the window. A tile
@@ -811,7 +819,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r)
           if (!(r0 + r >= rmin && r0 + r < rlim &&
-                (sh.window <= 0 || qpos_s[r0 + r] - kpos < sh.window)))
+                (sh.window <= 0 || dist + qpos_s[r0 + r] < sh.window)))
             x[r] = -INFINITY;
       }
       if (xs != nullptr) {
@@ -933,7 +941,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_row_ld<NH>(tmem + lane_off + C::TM_O + r0, o);
           tc_fence_before();
           const int seg = w.b * p.H_kv + hk;
-          const bool whole = t0 == w.f && w.seg_end();
+          const bool whole = t0 + 1 == w.n && w.t == w.f;
           const size_t slot = static_cast<size_t>((w.b + grp) * p.H_kv + hk) * R;
 #pragma unroll
           for (int rr = 0; rr < NH; ++rr) {
@@ -964,8 +972,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           if (sid == 0) {
-            if (t0 == w.f) dt.seg_first[seg] = grp;
-            if (w.seg_end()) dt.seg_last[seg] = grp;
+            if (t0 + 1 == w.n) dt.seg_first[seg] = grp;
+            if (w.t == w.f) dt.seg_last[seg] = grp;
           }
         }
       }
@@ -982,93 +990,133 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Merge of the partials of one output row per warp: LSE = ln sum_c exp(LSE_c),
-// O = sum_c exp(LSE_c - LSE) O_c over the pieces c of its segment
-// (agentalpha.top "flash attention" answer, follow-up 2). Segments inside
-// one CTA's range were written by that CTA; empty sequences get O = 0 and
-// LSE = -inf here.
-template <int D>
-__global__ void __launch_bounds__(256)
-    merge_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt) {
-  const long long rid = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  const int R = dec.n_rows;
-  if (rid >= static_cast<long long>(p.B) * p.H_kv * R) return;
-  const int seg = static_cast<int>(rid / R);
-  const int r = static_cast<int>(rid % R);
-  const int b = seg / p.H_kv;
-  const int hk = seg % p.H_kv;
-  const int len = __ldg(dec.cache_seqlens + b);
-  if (len < 0 || len > p.max_seqlen) return;   // reported by the partials kernel
-  const size_t orow = static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H + hk * dec.g +
-                      r % dec.g;
-  constexpr int PER = D / 32;   // columns per lane
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + orow * D + lane * PER;
-  float acc[PER];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+// Range of group partials [c0, c1] of a segment; false when its CTA wrote the rows
+// (one piece) or the sequence is empty.
+struct Pieces {
+  int c0, c1;
+};
+__device__ __forceinline__ Pieces seg_pieces(const DecodeTArgs& dt, int seg, int len) {
+  if (len <= 0) return {0, -1};
+  return {dt.seg_first[seg], dt.seg_last[seg]};
+}
+
+// LSE of row r over the pieces (group c's sits in slot (b + c) H_kv + hk).
+__device__ __forceinline__ float pieces_lse(const DecodeTArgs& dt, const Pieces& pc, int b, int hk,
+                                            int H_kv, int R, int r) {
   float m = -INFINITY, tot = 0.f;
-  if (len > 0) {
-    const int c0 = dt.seg_first[seg];
-    const int c1 = dt.seg_last[seg];
-    if (c0 == c1) return;   // one piece: its CTA wrote the row
-    if (c0 < 0 || c1 >= dt.ctas / p.H_kv || c0 > c1) {
+  for (int c = pc.c0; c <= pc.c1; ++c)
+    m = fmaxf(m, dt.lse_part[static_cast<size_t>((b + c) * H_kv + hk) * R + r]);
+  if (m == -INFINITY) return m;
+  for (int c = pc.c0; c <= pc.c1; ++c)
+    tot += expf(dt.lse_part[static_cast<size_t>((b + c) * H_kv + hk) * R + r] - m);
+  return m + logf(tot);
+}
+
+__device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// What follows the ranges, in one launch. Blocks [0, merge_blocks): the merge of the
+// partials, one output row per warp: LSE = ln sum_c exp(LSE_c), O = sum_c exp(LSE_c -
+// LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
+// get O = 0 and LSE = -inf here. The others: key_weights[b, hk, j] += sum_r 2^(z_rj -
+// LSE_r log2 e), four tiles of a segment per block, a warp a tile, four slots a lane.
+constexpr int FIN_THREADS = 128;
+template <int D>
+__global__ void __launch_bounds__(FIN_THREADS)
+    finish_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt,
+                  const DecodeShapeArgs sh, const Lens seqs, const float* __restrict__ xs,
+                  int merge_blocks, int tiles_max) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int R = dec.n_rows;
+  if (static_cast<int>(blockIdx.x) < merge_blocks) {
+    const long long rid = static_cast<long long>(blockIdx.x) * (FIN_THREADS / 32) + warp;
+    wait_primary();
+    if (rid >= static_cast<long long>(p.B) * p.H_kv * R) return;
+    const int seg = static_cast<int>(rid / R);
+    const int r = static_cast<int>(rid % R);
+    const int b = seg / p.H_kv;
+    const int hk = seg % p.H_kv;
+    const int len = __ldg(dec.cache_seqlens + b);
+    if (len < 0 || len > p.max_seqlen) return;   // reported by the partials kernel
+    const Pieces pc = seg_pieces(dt, seg, len);
+    if (len > 0 && pc.c0 == pc.c1) return;   // one piece: its CTA wrote the row
+    if (len > 0 && (pc.c0 < 0 || pc.c1 >= dt.ctas / p.H_kv || pc.c0 > pc.c1)) {
       if (lane == 0) record_bounds(p.err, BAD_MERGE);
       return;
     }
-    // Group c's piece of the segment sits in slot (b + c) H_kv + hk.
-    for (int c = c0 + lane; c <= c1; c += 32)
+    const size_t orow = static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H + hk * dec.g +
+                        r % dec.g;
+    constexpr int PER = D / 32;   // columns per lane
+    float acc[PER] = {};
+    float m = -INFINITY, tot = 0.f;
+    for (int c = pc.c0 + lane; c <= pc.c1; c += 32)
       m = fmaxf(m, dt.lse_part[static_cast<size_t>((b + c) * p.H_kv + hk) * R + r]);
 #pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, sh));
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, s));
     if (m != -INFINITY) {
-      for (int c = c0; c <= c1; ++c) {
-        const size_t prow = static_cast<size_t>((b + c) * p.H_kv + hk) * R + r;
-        const float ls = dt.lse_part[prow];
-        if (ls == -INFINITY) continue;
-        const float wgt = expf(ls - m);
-        tot += wgt;
-        const float* src = dt.o_part + prow * D + lane * PER;
+      for (int c0 = pc.c0; c0 <= pc.c1; c0 += 32) {
+        // The 32 weights at once, a lane each; the rows then come without waiting.
+        const int c = c0 + lane;
+        const float mine =
+            c <= pc.c1 ? expf(dt.lse_part[static_cast<size_t>((b + c) * p.H_kv + hk) * R + r] - m) : 0.f;
+        const int cnt = min(32, pc.c1 - c0 + 1);
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k) {
+          const float wgt = __shfl_sync(FULL, mine, k);
+          const float* src =
+              dt.o_part + (static_cast<size_t>((b + c0 + k) * p.H_kv + hk) * R + r) * D + lane * PER;
+          tot += wgt;
 #pragma unroll
-        for (int k = 0; k < PER; k += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + k);
-          acc[k] += wgt * v.x;
-          acc[k + 1] += wgt * v.y;
+          for (int e = 0; e < PER; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + e);
+            acc[e] = fmaf(wgt, v.x, acc[e]);
+            acc[e + 1] = fmaf(wgt, v.y, acc[e + 1]);
+          }
         }
       }
     }
-  }
-  const float inv = (tot > 0.f) ? 1.f / tot : 0.f;
+    const float inv = (tot > 0.f) ? 1.f / tot : 0.f;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + orow * D + lane * PER;
 #pragma unroll
-  for (int k = 0; k < PER; k += 2)
-    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0) p.lse[orow] = (tot > 0.f) ? m + logf(tot) : -INFINITY;
-}
-
-// key_weights[b, hk, j] += sum_r 2^(z_rj - LSE_r log2 e), one CTA per tile of a
-// segment, one thread per slot.
-__global__ void __launch_bounds__(BN)
-    weights_kernel(const AttnParams p, const DecodeArgs dec, const DecodeShapeArgs sh,
-                   const Lens seqs, const float* __restrict__ xs, int tiles_max) {
+    for (int e = 0; e < PER; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) p.lse[orow] = (tot > 0.f) ? m + logf(tot) : -INFINITY;
+    return;
+  }
   __shared__ float lse2[64];
-  const int t = static_cast<int>(blockIdx.x % tiles_max);
-  const size_t seg = blockIdx.x / tiles_max;
-  const int b = static_cast<int>(seg / p.H_kv), hk = static_cast<int>(seg % p.H_kv);
+  const int quads = (tiles_max + 3) / 4;
+  const int id = static_cast<int>(blockIdx.x) - merge_blocks;
+  const int seg = id / quads;
+  const int b = seg / p.H_kv, hk = seg % p.H_kv;
   int f, len;
   const int n = seq_tiles(seqs, b, f, len);
-  if (t < f || t >= n) return;
-  const int R = dec.n_rows, j = t * BN + threadIdx.x;
+  const int t = (id % quads) * 4 + warp;
+  if ((id % quads) * 4 >= n || (id % quads) * 4 + 3 < f) return;
+  wait_primary();
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
-    const float v = p.lse[static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H + hk * dec.g + r % dec.g];
+    const Pieces pc = seg_pieces(dt, seg, len);
+    const float v = pc.c0 == pc.c1 ? p.lse[static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H +
+                                           hk * dec.g + r % dec.g]
+                                   : pieces_lse(dt, pc, b, hk, p.H_kv, R, r);
     lse2[r] = v == -INFINITY ? 0.f : v * LOG2E;   // a row that sees nothing: its z are -inf
   }
   __syncthreads();
-  if (j >= len) return;
-  const float* x = xs + (seg * tiles_max + t) * R * BN + threadIdx.x;
-  float w = 0.f;
-  for (int r = 0; r < R; ++r) w += ex2_approx(x[static_cast<size_t>(r) * BN] - lse2[r]);
-  sh.key_weights[seg * sh.slots + j] += w;
+  if (t < f || t >= n) return;
+  const float* x = xs + (static_cast<size_t>(seg) * tiles_max + t) * R * BN + 4 * lane;
+  float w[4] = {};
+#pragma unroll 4
+  for (int r = 0; r < R; ++r) {
+    const float4 v = *reinterpret_cast<const float4*>(x + static_cast<size_t>(r) * BN);
+    const float e = lse2[r];
+    w[0] += ex2_approx(v.x - e);
+    w[1] += ex2_approx(v.y - e);
+    w[2] += ex2_approx(v.z - e);
+    w[3] += ex2_approx(v.w - e);
+  }
+  float* dst = sh.key_weights + static_cast<size_t>(seg) * sh.slots + t * BN + 4 * lane;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t * BN + 4 * lane + k < len) dst[k] += w[k];
 }
 
 struct Workspace {
@@ -1139,15 +1187,23 @@ cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShape
     e = launch_nq<D, 64>(tq, tk, tv, p, d, sh, w, seqs, stream);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.H_kv * d.n_rows;
-  if ((rows + 7) / 8 > INT_MAX) return cudaErrorInvalidConfiguration;
-  merge_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p, d, w.t);
-  if ((e = cudaGetLastError()) != cudaSuccess || sh.key_weights == nullptr) return e;
   const int tiles_max = (p.max_seqlen + BN - 1) / BN;
-  const long long blocks = static_cast<long long>(p.B) * p.H_kv * tiles_max;
+  const long long merge = (rows + FIN_THREADS / 32 - 1) / (FIN_THREADS / 32);
+  const long long blocks =
+      merge + (sh.key_weights ? static_cast<long long>(p.B) * p.H_kv * ((tiles_max + 3) / 4) : 0);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  if (blocks > 0)
-    weights_kernel<<<static_cast<unsigned>(blocks), BN, 0, stream>>>(p, d, sh, seqs, w.xs, tiles_max);
-  return cudaGetLastError();
+  // Launched while the ranges still run; it waits for them before it reads.
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(FIN_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, finish_kernel<D>, p, d, w.t, sh, seqs,
+                            static_cast<const float*>(w.xs), static_cast<int>(merge), tiles_max);
 }
 
 }  // namespace sdec
