@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -46,7 +47,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _shape(q: torch.Tensor, k: torch.Tensor, cu_seqlens, max_seqlen):
@@ -71,14 +73,19 @@ def _shape(q: torch.Tensor, k: torch.Tensor, cu_seqlens, max_seqlen):
     return cu_seqlens.numel() - 1, 0, H, k.shape[1], D, int(max_seqlen), T
 
 
-@contextlib.contextmanager
-def _on(device: torch.device):
-    """The tensors' device as the current one: the library launches there."""
+def _call(what: str, fn, device: torch.device, *args) -> None:
+    """``fn(*args)`` with the tensors' device as the current one: the library launches there."""
     if device.index is None or device.index == torch.cuda.current_device():
-        yield
+        st = fn(*args)
     else:
         with torch.cuda.device(device):
-            yield
+            st = fn(*args)
+    if st:
+        _abi.check(st, what)
+
+
+def _is(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> bool:
+    return t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()
 
 
 def _aux(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
@@ -86,8 +93,8 @@ def _aux(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
     """Pointer of an optional side tensor after its checks."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    if not _is(t, shape, dtype, device):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
@@ -95,20 +102,30 @@ def _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end):
     """fa_score_shape of the arguments, or None when none is given."""
     if softcap is None and alibi_slopes is None and key_begin is None and key_end is None:
         return None
-    tokens = (q.shape[0],) if cu_seqlens is not None else tuple(q.shape[:2])
+    shape, device = q.shape, q.device
+    tokens = shape[:1] if cu_seqlens is not None else shape[:2]
+    if cu_seqlens is not None and (cu_seqlens.device != device or not cu_seqlens.is_contiguous()):
+        raise ValueError(f"cu_seqlens must be contiguous on {device}")
     return _abi.ScoreShape(
         0.0 if softcap is None else float(softcap),
-        _aux(alibi_slopes, "alibi_slopes", torch.float32, (q.shape[-2],), q.device),
-        _aux(key_begin, "key_begin", torch.int32, tokens, q.device),
-        _aux(key_end, "key_end", torch.int32, tokens, q.device))
+        _aux(alibi_slopes, "alibi_slopes", torch.float32, shape[-2:-1], device),
+        _aux(key_begin, "key_begin", torch.int32, tokens, device),
+        _aux(key_end, "key_end", torch.int32, tokens, device))
 
 
 def _same(what: str, like: torch.Tensor, **tensors):
     """Shape, type, layout and device of ``tensors`` are those of ``like``."""
+    shape, dtype, device = like.shape, like.dtype, like.device
     for name, t in tensors.items():
-        if (t.shape != like.shape or t.dtype != like.dtype or not t.is_contiguous() or
-                t.device != like.device):
+        if not _is(t, shape, dtype, device):
             raise ValueError(f"{name} must match {what} in shape, dtype and device and be contiguous")
+
+
+def _beside(q: torch.Tensor, k: torch.Tensor):
+    """k differs from q in its heads only."""
+    a, b = q.shape, k.shape
+    if k.device != q.device or k.dtype is not q.dtype or a[-1] != b[-1] or a[:-2] != b[:-2]:
+        raise ValueError("k must match q but for its heads")
 
 
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
@@ -128,26 +145,24 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = Fal
     B, N, H, H_kv, D, max_sl, T = _shape(q, k, cu_seqlens, max_seqlen)
     if v.shape != k.shape or v.dtype != q.dtype or k.dtype != q.dtype:
         raise ValueError("k and v must match in shape and dtype with q's dtype")
+    shape = _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end)
+    rows = (B, H, N) if cu_seqlens is None else (H, T)
+    if shape is not None:
+        _beside(q, k)
+        _same("k", k, v=v)
+        if out is not None:
+            _same("q", q, out=out)
+        _aux(lse, "lse", torch.float32, rows, q.device)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, H, N) if cu_seqlens is None else (H, T), device=q.device,
-                          dtype=torch.float32)
+        lse = torch.empty(rows, device=q.device, dtype=torch.float32)
     s = -1.0 if scale is None else float(scale)
-    shape = _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end)
     if shape is not None:
-        _same("k", k, v=v)
-        _same("q", q, out=out)
-        _aux(lse, "lse", torch.float32, (B, H, N) if cu_seqlens is None else (H, T), q.device)
-        if k.device != q.device or q.dtype != k.dtype or k.shape[-1] != D or k.dim() != q.dim() or \
-                k.shape[:-2] != q.shape[:-2]:
-            raise ValueError("k must match q but for its heads")
-        with _on(q.device):
-            st = _lib().fa_fwd_shaped(
-                _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, H_kv, N, D,
-                _DTYPES[q.dtype], int(bool(causal)), s, _ptr(cu_seqlens), max_sl, T,
-                ctypes.byref(shape), _stream(q.device))
-        _abi.check(st, "fa_fwd_shaped")
+        _call("fa_fwd_shaped", _lib().fa_fwd_shaped, q.device, q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, H_kv, N, D, _DTYPES[q.dtype],
+              int(bool(causal)), s, _ptr(cu_seqlens), max_sl, T, ctypes.byref(shape),
+              _stream(q.device))
         return out, lse
     st = _lib().fa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, H_kv, N, D,
                            _DTYPES[q.dtype], int(bool(causal)), s, _ptr(cu_seqlens), max_sl, T,
@@ -189,30 +204,28 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     for t in (dout, o, v, lse):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
     shape = _score_shape(q, cu_seqlens, softcap, alibi_slopes, key_begin, key_end)
     if shape is not None:
         if phases != BWD_FUSED:
             raise ValueError("shaped scores have the BWD_FUSED backward only")
-        _same("q", q, dout=dout, o=o, dq=dq)
-        _same("k", k, v=v, dk=dk, dv=dv)
+        _beside(q, k)
+        _same("q", q, dout=dout, o=o, **({} if dq is None else {"dq": dq}))
+        _same("k", k, v=v, **{n: x for n, x in (("dk", dk), ("dv", dv)) if x is not None})
         _aux(lse, "lse", torch.float32, (B, H, N) if cu_seqlens is None else (H, T), q.device)
-        if k.device != q.device or q.dtype != k.dtype or k.shape[-1] != D or k.dim() != q.dim() or \
-                k.shape[:-2] != q.shape[:-2]:
-            raise ValueError("k must match q but for its heads")
-        need = int(_lib().fa_bwd_shaped_workspace_size(T, B, H, D, _DTYPES[q.dtype]))
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if shape is not None:
+        dtype = _DTYPES[q.dtype]
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        with _on(q.device):
-            st = _lib().fa_bwd_shaped(
-                _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-                _ptr(dv), B, H, H_kv, N, D, _DTYPES[q.dtype], int(bool(causal)),
-                -1.0 if scale is None else float(scale), _ptr(cu_seqlens), max_sl, T,
-                ctypes.byref(shape), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                _stream(q.device))
-        _abi.check(st, "fa_bwd_shaped")
+            workspace = torch.empty(_lib().fa_bwd_shaped_workspace_size(T, B, H, D, dtype),
+                                    dtype=torch.uint8, device=q.device)
+        _call("fa_bwd_shaped", _lib().fa_bwd_shaped, q.device, q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
+              dk.data_ptr(), dv.data_ptr(), B, H, H_kv, N, D, dtype, int(bool(causal)),
+              -1.0 if scale is None else float(scale), _ptr(cu_seqlens), max_sl, T,
+              ctypes.byref(shape), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _stream(q.device))
         return dq, dk, dv
     need = workspace_size(T, H, D, q.dtype, phases)
     if workspace is None:
@@ -263,12 +276,10 @@ def key_ranges(N: Optional[int] = None, *, B: int = 1, causal: bool = True,
     docs = _aux(doc_ids, "doc_ids", torch.int32, tokens, device)
     prefix = _aux(prefix_lens, "prefix_lens", torch.int32, (B,), device)
     begin, end = (torch.empty(tokens, dtype=torch.int32, device=device) for _ in range(2))
-    with _on(device):
-        st = _lib().fa_key_ranges(docs, prefix, 0 if window is None else int(window),
-                                  int(bool(causal)), B, 0 if cu_seqlens is not None else N,
-                                  _ptr(cu_seqlens), int(max_seqlen or 0), N, _ptr(begin),
-                                  _ptr(end), _stream(device))
-    _abi.check(st, "fa_key_ranges")
+    _call("fa_key_ranges", _lib().fa_key_ranges, device, docs, prefix,
+          0 if window is None else int(window), int(bool(causal)), B,
+          0 if cu_seqlens is not None else N, _ptr(cu_seqlens), int(max_seqlen or 0), N,
+          begin.data_ptr(), end.data_ptr(), _stream(device))
     return begin, end
 
 
@@ -317,15 +328,15 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if block_table is None and page_size is None:
         page_size = rows // max(B, 1)
     max_blocks = block_table.shape[1] if block_table is not None else 0
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((q.shape[0], H), device=q.device, dtype=torch.float32)
     if not (softcap is None and alibi_slopes is None and window is None and
             key_positions is None and key_weights is None):
         return _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, block_table,
                               page_size, causal, scale, n_split, out, lse, workspace, softcap,
                               alibi_slopes, window, key_positions, key_weights)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((q.shape[0], H), device=q.device, dtype=torch.float32)
     need = decode_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k, n_split)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
@@ -340,15 +351,21 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 def _check_cache(k_cache, v_cache, cache_seqlens, block_table):
     """Device, type and layout of a cache as decode and evict take it."""
-    dev = k_cache.device
-    if k_cache.dim() != 3 or k_cache.dtype != torch.bfloat16 or not k_cache.is_cuda or \
-            not k_cache.is_contiguous():
+    dev, shape = k_cache.device, k_cache.shape
+    if len(shape) != 3 or dev.type != "cuda" or not _is(k_cache, shape, torch.bfloat16, dev):
         raise ValueError("a cache is a contiguous bfloat16 CUDA tensor [rows, H_kv, D]")
-    _same("k_cache", k_cache, v_cache=v_cache)
-    _aux(cache_seqlens, "cache_seqlens", torch.int32, tuple(cache_seqlens.shape), dev)
+    if not _is(v_cache, shape, torch.bfloat16, dev):
+        raise ValueError("v_cache must match k_cache in shape, dtype and device and be contiguous")
+    B = cache_seqlens.numel()
+    _aux(cache_seqlens, "cache_seqlens", torch.int32, (B,), dev)
     if block_table is not None:
-        _aux(block_table, "block_table", torch.int32,
-             (cache_seqlens.numel(), block_table.shape[-1]), dev)
+        _aux(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_shaped_need(lib, device, B, q_len, H, H_kv, D, max_seqlen_k, weights) -> int:
+    """fa_decode_shaped_workspace_size on the current device (``device`` keys the cache)."""
+    return lib.fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k, weights)
 
 
 def _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, block_table, page_size,
@@ -356,34 +373,45 @@ def _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, bloc
                    key_positions, key_weights):
     if n_split != 0:
         raise ValueError("shaped scores take automatic splits only (n_split = 0)")
-    B, (_, H, D) = cache_seqlens.numel(), q.shape
-    rows, H_kv = k_cache.shape[:2]
-    dev = q.device
+    B, (tokens, H, D), dev = cache_seqlens.numel(), q.shape, q.device
+    rows, H_kv, D_kv = k_cache.shape
     _check_cache(k_cache, v_cache, cache_seqlens, block_table)
-    if k_cache.device != dev or k_cache.shape[2] != D or q.dtype != torch.bfloat16 or \
-            not q.is_contiguous() or q.shape[0] != B * q_len:
+    if k_cache.device != dev or D_kv != D or tokens != B * q_len or \
+            not _is(q, q.shape, torch.bfloat16, dev):
         raise ValueError("q must be a contiguous bfloat16 tensor [B * q_len, H, D] beside the cache")
-    _same("q", q, out=out)
-    _aux(lse, "lse", torch.float32, (q.shape[0], H), dev)
-    slots = next((t.shape[-1] for t in (key_weights, key_positions) if t is not None), 0)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _same("q", q, out=out)
+    if lse is None:
+        lse = torch.empty((tokens, H), device=dev, dtype=torch.float32)
+    else:
+        _aux(lse, "lse", torch.float32, (tokens, H), dev)
+    slots = (key_weights.shape[-1] if key_weights is not None else
+             key_positions.shape[-1] if key_positions is not None else 0)
+    side = (B, H_kv, slots)
     shape = _abi.DecodeShape(
         0.0 if softcap is None else float(softcap),
         _aux(alibi_slopes, "alibi_slopes", torch.float32, (H,), dev),
         0 if window is None else int(window),
-        _aux(key_positions, "key_positions", torch.int32, (B, H_kv, slots), dev),
-        _aux(key_weights, "key_weights", torch.float32, (B, H_kv, slots), dev), slots)
-    with _on(dev):
-        need = int(_lib().fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k,
-                                                          int(key_weights is not None)))
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-        st = _lib().fa_decode_shaped(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cache_seqlens),
-            _ptr(block_table), B, int(q_len), H, H_kv, D, int(page_size),
-            0 if block_table is None else block_table.shape[1], rows, int(max_seqlen_k),
-            int(bool(causal)), -1.0 if scale is None else float(scale), ctypes.byref(shape),
-            _ptr(workspace) if need else None, need, _stream(dev))
-    _abi.check(st, "fa_decode_shaped")
+        _aux(key_positions, "key_positions", torch.int32, side, dev),
+        _aux(key_weights, "key_weights", torch.float32, side, dev), slots)
+    lib = _lib()
+    if dev.index == torch.cuda.current_device():
+        need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, max_seqlen_k,
+                                   int(key_weights is not None))
+    else:
+        with torch.cuda.device(dev):
+            need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, max_seqlen_k,
+                                       int(key_weights is not None))
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    _call("fa_decode_shaped", lib.fa_decode_shaped, dev, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), cache_seqlens.data_ptr(),
+          _ptr(block_table), B, int(q_len), H, H_kv, D, int(page_size),
+          0 if block_table is None else block_table.shape[1], rows, int(max_seqlen_k),
+          int(bool(causal)), -1.0 if scale is None else float(scale), ctypes.byref(shape),
+          workspace.data_ptr() if need else None, need, _stream(dev))
     return out, lse
 
 
@@ -426,28 +454,27 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_seqlens: torch.Ten
         if out_block_table is not None:
             raise ValueError("a paged cache needs out_page_size")
         out_page_size = k_out.shape[0] // max(B, 1)
-    _check_cache(k_out, v_out, cache_seqlens, out_block_table)
     if k_out.device != dev or k_out.shape[1:] != k_cache.shape[1:]:
         raise ValueError("k_out must have the cache's heads, head size and device")
+    _check_cache(k_out, v_out, cache_seqlens, out_block_table)
     slots = key_weights.shape[-1]
     w = _aux(key_weights, "key_weights", torch.float32, (B, H_kv, slots), dev)
     pos = _aux(key_positions, "key_positions", torch.int32, (B, H_kv, slots), dev)
     seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
     weights = torch.empty((B, H_kv, out_slots), dtype=torch.float32, device=dev)
     positions = torch.empty((B, H_kv, out_slots), dtype=torch.int32, device=dev)
-    need = int(_lib().fa_cache_evict_workspace_size(B, H_kv, int(keep)))
+    lib = _lib()
+    need = lib.fa_cache_evict_workspace_size(B, H_kv, int(keep))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    with _on(dev):
-        st = _lib().fa_cache_evict(
-            _ptr(k_cache), _ptr(v_cache), _ptr(cache_seqlens), _ptr(block_table), B, H_kv, D,
-            int(page_size), 0 if block_table is None else block_table.shape[1], rows,
-            int(max_seqlen_k), w, pos, slots, int(keep), int(recent), _ptr(k_out), _ptr(v_out),
-            _ptr(out_block_table), int(out_page_size),
-            0 if out_block_table is None else out_block_table.shape[1], k_out.shape[0],
-            _ptr(seqlens), _ptr(weights), _ptr(positions), out_slots, _ptr(workspace), need,
-            _stream(dev))
-    _abi.check(st, "fa_cache_evict")
+    _call("fa_cache_evict", lib.fa_cache_evict, dev, k_cache.data_ptr(), v_cache.data_ptr(),
+          cache_seqlens.data_ptr(), _ptr(block_table), B, H_kv, D, int(page_size),
+          0 if block_table is None else block_table.shape[1], rows, int(max_seqlen_k), w, pos,
+          slots, int(keep), int(recent), k_out.data_ptr(), v_out.data_ptr(),
+          _ptr(out_block_table), int(out_page_size),
+          0 if out_block_table is None else out_block_table.shape[1], k_out.shape[0],
+          seqlens.data_ptr(), weights.data_ptr(), positions.data_ptr(), out_slots,
+          workspace.data_ptr(), need, _stream(dev))
     return k_out, v_out, seqlens, weights, positions
 
 

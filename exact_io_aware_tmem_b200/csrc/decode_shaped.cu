@@ -1154,8 +1154,7 @@ cudaError_t launch_nq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh,
                       const Workspace& w, const Lens& seqs, cudaStream_t stream) {
   using C = Cfg<D, NQ>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      decode_shaped_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t e = allow_smem<decode_shaped_kernel<D, NQ>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const CapArgs cap = sh.cap > 0.f ? cap_args(sh.cap, p.scale) : CapArgs{};
   decode_shaped_kernel<D, NQ><<<static_cast<unsigned>(w.t.ctas), THREADS, C::SMEM, stream>>>(

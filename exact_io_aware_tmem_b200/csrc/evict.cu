@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictArgs a) {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int held = std::min(a.max_len, KEYS_MAX);
-  const cudaError_t e = cudaFuncSetAttribute(
-      select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, KEYS_MAX * 4);
+  const cudaError_t e = allow_smem<select_kernel>(KEYS_MAX * 4);
   if (e != cudaSuccess) return e;
   select_kernel<<<a.B * a.H_kv, SELECT_THREADS, held * sizeof(unsigned), stream>>>(a, held);
   const long long n = static_cast<long long>(a.B) * a.keep * a.H_kv * (a.D / 8);

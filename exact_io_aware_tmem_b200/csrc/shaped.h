@@ -6,6 +6,8 @@
 // key j visible to query i iff begin_i <= j < end_i (and j <= i when causal).
 #pragma once
 
+#include <atomic>
+
 #include "params.h"
 
 namespace fa {
@@ -92,6 +94,21 @@ __device__ __forceinline__ long long cache_row(const int* table, int max_blocks,
 __device__ __forceinline__ void record_bounds(const DevErr& e, unsigned where) {
   atomicOr(e.word, ERR_BOUNDS);
   atomicExch(e.word + 1, where);
+}
+
+// Host: lets ``Kernel`` have up to ``bytes`` of dynamic shared memory, once per device.
+template <auto Kernel>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  const cudaError_t got = cudaGetDevice(&dev);
+  if (got != cudaSuccess) return got;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 cudaError_t launch_shaped_fwd_simt(const AttnParams& p, const ShapeArgs& sh, bool f32,

@@ -774,8 +774,7 @@ cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, int2* tiles, cudaSt
       !make_tmap_bf16_3d(&tg, p.dout, p.total, p.H, D, 1, BT) ||
       !make_tmap_f32_2d(&ta, p.dq_accum, p.total, static_cast<unsigned long long>(p.H) * D, 32, 32))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(shaped_bwd_kernel<D, CAP, BIAS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = allow_smem<shaped_bwd_kernel<D, CAP, BIAS>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const bool ranged = sh.key_begin != nullptr || sh.key_end != nullptr;
   if (ranged) {

@@ -684,8 +684,7 @@ cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream
       !make_tmap_bf16_2d(&tk, p.k, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN) ||
       !make_tmap_bf16_2d(&tv, p.v, p.total, static_cast<unsigned long long>(p.H_kv) * D, 64, BN))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(shaped_fwd_kernel<D, MODE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t e = allow_smem<shaped_fwd_kernel<D, MODE>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int group = l2_group(4ll * p.max_seqlen * D, p.H / p.H_kv, p.H * p.B);
   const CapArgs cap = MODE >= CAPPED ? cap_args(sh.cap, p.scale) : CapArgs{};
