@@ -111,10 +111,9 @@ inline cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-cudaError_t launch_shaped_fwd_simt(const AttnParams& p, const ShapeArgs& sh, bool f32,
-                                   cudaStream_t stream);
-cudaError_t launch_shaped_bwd_simt(const AttnParams& p, const ShapeArgs& sh, bool f32,
-                                   cudaStream_t stream);
+// float32 (shaped_f32.cu).
+cudaError_t launch_shaped_fwd_f32(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
+cudaError_t launch_shaped_bwd_f32(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_fwd.cu).
 cudaError_t launch_shaped_fwd(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_bwd.cu): p.delta and p.dq_accum as for the fused

@@ -66,7 +66,7 @@ fa_status fa_fwd_shaped(const void* q, const void* k, const void* v, void* o, fl
   if (p.err.word == nullptr) return FA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const fa::ShapeArgs a = fa::shape_args(*shape, p.scale);
-  return fa::record_cuda(dtype == FA_F32 ? fa::launch_shaped_fwd_simt(p, a, true, s)
+  return fa::record_cuda(dtype == FA_F32 ? fa::launch_shaped_fwd_f32(p, a, s)
                                          : fa::launch_shaped_fwd(p, a, s));
 }
 
@@ -113,7 +113,7 @@ fa_status fa_bwd_shaped(const void* q, const void* k, const void* v, const void*
   if (p.err.word == nullptr) return FA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const fa::ShapeArgs a = fa::shape_args(*shape, p.scale);
-  if (dtype == FA_F32) return fa::record_cuda(fa::launch_shaped_bwd_simt(p, a, true, s));
+  if (dtype == FA_F32) return fa::record_cuda(fa::launch_shaped_bwd_f32(p, a, s));
   // D_i, the dQ accumulator, the query tiles' ranges.
   const size_t rows = static_cast<size_t>(p.total) * H;
   ws += fa::round256(rows * sizeof(float));
