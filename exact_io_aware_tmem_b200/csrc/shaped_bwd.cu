@@ -216,7 +216,8 @@ __device__ __forceinline__ void probs(const uint32_t (&sr)[32], const float* lse
   const bool right = d0 < 0;
   const float sl = right ? slope2 : -slope2;
   const bool mixed = BIAS && __any_sync(FULL, d0 < 0 && d0 + 31 > 0);
-  const float base = BIAS ? sl * static_cast<float>(d0) : 0.f;
+  const float d0f = static_cast<float>(d0);
+  const float base = BIAS ? sl * d0f : 0.f;
   const float4* lse4 = reinterpret_cast<const float4*>(lse);
 #pragma unroll
   for (int q = 0; q < 32; q += 2) {
@@ -226,8 +227,8 @@ __device__ __forceinline__ void probs(const uint32_t (&sr)[32], const float* lse
     if (BIAS) {
       float2 bias;
       if (mixed)
-        bias = make_float2(-slope2 * fabsf(static_cast<float>(d0 + q)),
-                           -slope2 * fabsf(static_cast<float>(d0 + q + 1)));
+        bias = make_float2(-slope2 * fabsf(d0f + static_cast<float>(q)),
+                           -slope2 * fabsf(d0f + static_cast<float>(q + 1)));
       else
         bias = __ffma2_rn(make_float2(sl, sl), make_float2(static_cast<float>(q), static_cast<float>(q + 1)),
                           make_float2(base, base));

@@ -48,13 +48,7 @@ namespace sfwd {
 
 constexpr int BM = 128;
 constexpr int BN = 128;
-constexpr int SOFTMAX_WARPS = 16;  // two query tiles x two halves of 64 keys x four lane quarters
-constexpr int THREADS = 32 * SOFTMAX_WARPS + 64;
-constexpr int WARP_TMA = 16;
-constexpr int WARP_MMA = 17;
-constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;
-constexpr uint32_t TM_O = 256;
 constexpr uint32_t SPAN = 128 * 128;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float HIGH_LOG2 = 64.f;     // largest z - m that is taken as it is
@@ -65,20 +59,30 @@ constexpr float LN2 = 0.69314718055994531f;
 
 template <int D>
 struct Cfg {
+  static constexpr int G = D == 128 ? 2 : 1;         // query tiles per CTA
+  static constexpr int CTAS = D == 128 ? 1 : 2;      // CTAs per SM
+  // Query tiles x two halves of 64 keys x four lane quarters.
+  static constexpr int SOFTMAX_WARPS = 8 * G;
+  static constexpr int THREADS = 32 * SOFTMAX_WARPS + 64;
+  static constexpr int WARP_TMA = SOFTMAX_WARPS;
+  static constexpr int WARP_MMA = SOFTMAX_WARPS + 1;
+  static constexpr uint32_t TM_O = G * 128;
+  static constexpr uint32_t TMEM_COLS = 256 * G;
+  static_assert(TM_O + G * D <= TMEM_COLS && CTAS * TMEM_COLS <= 512, "TMEM budget");
   static constexpr uint32_t TILE = BM * D * 2;
-  static constexpr int KS = D == 128 ? 3 : 4;
-  static constexpr int VS = D == 128 ? 2 : 4;
+  static constexpr int KS = 3;
+  static constexpr int VS = 2;
   static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
+  static constexpr uint32_t OFF_K = OFF_Q + G * TILE;
   static constexpr uint32_t OFF_V = OFF_K + KS * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + VS * TILE;
   // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2],
   // p_ready[2], o_full
   static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;   // tmem slot, abort, lo[2], hi[2]
-  static constexpr uint32_t OFF_ROW = OFF_MISC + 32;   // float [2 halves][2 BM]: row maxima, sums
-  static constexpr uint32_t SMEM = OFF_ROW + 2 * 2 * BM * 4;
-  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr uint32_t OFF_ROW = OFF_MISC + 32;   // float [2 halves][G BM]: row maxima, sums
+  static constexpr uint32_t SMEM = OFF_ROW + 2 * G * BM * 4;
+  static_assert(CTAS == 1 ? SMEM <= 232448 : 2 * (SMEM + 1024) <= 233472, "shared memory budget");
 };
 
 template <int D>
@@ -190,15 +194,16 @@ __device__ __forceinline__ void chunk(const uint32_t (&r)[16], int lo, int hi, i
   constexpr bool BIAS = has_bias(MODE);
   const float sl = d0 >= 0 ? -slope2 : slope2;
   const bool mixed = PARTIAL && BIAS && __any_sync(FULL, d0 < 0 && d0 + 15 > 0);
-  const float base = BIAS ? fmaf(sl, static_cast<float>(d0), -m) : -m;
+  const float d0f = static_cast<float>(d0);
+  const float base = BIAS ? fmaf(sl, d0f, -m) : -m;
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const float2 s = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
     float2 add = make_float2(base, base);
     if (BIAS) {
       if (mixed) {
-        add.x = fmaf(-slope2, fabsf(static_cast<float>(d0 + i)), -m);
-        add.y = fmaf(-slope2, fabsf(static_cast<float>(d0 + i + 1)), -m);
+        add.x = fmaf(-slope2, fabsf(d0f + static_cast<float>(i)), -m);
+        add.y = fmaf(-slope2, fabsf(d0f + static_cast<float>(i + 1)), -m);
       } else {
         add = __ffma2_rn(make_float2(sl, sl),
                          make_float2(static_cast<float>(i), static_cast<float>(i + 1)), add);
@@ -279,15 +284,17 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     shaped_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const AttnParams p,
-                      const ShapeArgs sh, const CapArgs cap, int num_m2, int group) {
+                      const ShapeArgs sh, const CapArgs cap, int num_m, int group) {
   using C = Cfg<D>;
   constexpr bool BIAS = has_bias(MODE);
   constexpr bool FIXED = MODE == CAPPED_FIXED;
-  constexpr int KS = C::KS, VS = C::VS;
+  constexpr int KS = C::KS, VS = C::VS, G = C::G;
+  constexpr int SOFTMAX_WARPS = C::SOFTMAX_WARPS, WARP_TMA = C::WARP_TMA, WARP_MMA = C::WARP_MMA;
+  constexpr uint32_t TM_O = C::TM_O, TMEM_COLS = C::TMEM_COLS;
   constexpr uint32_t TILE = C::TILE, OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -297,12 +304,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   // Groups of heads for L2 reuse of K / V; inside a group the last query tiles
   // (the longest under a causal mask) first.
-  const TileSlot ts = grouped_slot(blockIdx.x, num_m2, p.H * p.B, group);
-  const int m2 = num_m2 - 1 - ts.t;
+  const TileSlot ts = grouped_slot(blockIdx.x, num_m, p.H * p.B, group);
+  const int mt = (num_m - 1 - ts.t) * G;   // first query tile
   const int h = ts.unit % p.H;
   const int b = ts.unit / p.H;
   const SeqInfo sq = seq_info(p, b);
-  if (!seq_ok(p, sq) || m2 * 2 * BM >= sq.len) return;   // whole CTA, before any shared state
+  if (!seq_ok(p, sq) || mt * BM >= sq.len) return;   // whole CTA, before any shared state
   const int hk = h / (p.H / p.H_kv);
 
   const Bars<D> bars{sbase + C::OFF_BAR};
@@ -315,10 +322,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // This thread's row (softmax warps) and its keys: warps 0-7 query tile 0, 8-15
   // tile 1; of each the first four the keys [0, 64) of a tile, the others the rest.
-  const int qpos = (m2 * 2 + (warp >> 3)) * BM + (warp & 3) * 32 + lane;
+  const int qpos = (mt + (warp >> 3)) * BM + (warp & 3) * 32 + lane;
   KeyRange kr = {0, 0};
   if (warp < SOFTMAX_WARPS && qpos < sq.len) kr = key_range(p, sh, sq, qpos);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == WARP_TMA * 32) {
     *abort = 0;
     s_lo[0] = s_lo[1] = INT_MAX;
     s_hi[0] = s_hi[1] = 0;
@@ -331,12 +338,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(bars.v_full(s), 1);
       mbar_init(bars.v_empty(s), 1);
     }
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < G; ++g) {
       mbar_init(bars.s_full(g), 1);
       mbar_init(bars.p_ready(g), 256);
     }
     mbar_init(bars.o_full(), 1);
     fence_mbar_init();
+    // Q does not wait for the ranges.
+    mbar_arrive_expect_tx(bars.q_full(), G * TILE);
+    for (int g = 0; g < G; ++g)
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_2d(sbase + OFF_Q + g * TILE + c * SPAN, &tm_q, bars.q_full(), h * D + c * 64,
+                    sq.start + (mt + g) * BM);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   if (warp == WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
@@ -360,9 +375,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the keys nearest to the queries, which the bias favours, then come first and set
   // the reference for good (91 against 127 us on B4 H16 N2048 D64); without one the
   // order makes no difference (571 us on B2 H16 N8192 D128 with a cap either way).
-  const bool any_0 = s_hi[0] > 0, any_1 = s_hi[1] > 0;
+  const bool any_0 = s_hi[0] > 0, any_1 = G > 1 && s_hi[1] > 0;
   const int t_0 = any_0 ? s_lo[0] / BN : INT_MAX, t_1 = any_1 ? s_lo[1] / BN : INT_MAX;
-  const int e_0 = (s_hi[0] + BN - 1) / BN, e_1 = (s_hi[1] + BN - 1) / BN;
+  const int e_0 = (s_hi[0] + BN - 1) / BN, e_1 = any_1 ? (s_hi[1] + BN - 1) / BN : 0;
   const int t0 = min(t_0, t_1), t1 = max(e_0, e_1);
   const int n_kv = t1 > 0 ? t1 - t0 : 0;
   const int b_0 = !any_0 ? 0 : BIAS ? t1 - e_0 : t_0 - t0;
@@ -373,13 +388,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == WARP_TMA) {
     // ------------------------------------------------------------ producer ---
     // The whole warp runs the loop; lane 0 issues the copies.
-    if (lane == 0 && n_kv > 0) {
-      mbar_arrive_expect_tx(bars.q_full(), 2 * TILE);
-      for (int g = 0; g < 2; ++g)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sbase + OFF_Q + g * TILE + c * SPAN, &tm_q, bars.q_full(), h * D + c * 64,
-                      sq.start + (2 * m2 + g) * BM);
-    }
     int jk = 0, jv = 0;
     long long t_last = clock64();
     while (jk < n_kv || jv < n_kv) {
@@ -428,6 +436,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     if (lane == 0) {
+      // Q has landed even where no key is seen.
+      if (n_kv == 0) mbar_wait(bars.q_full(), 0, p.err, abort, W_Q);
       // Drain: the tensor core's arrivals on the last stages' empty barriers
       // must land before the CTA's shared memory is released.
       for (int j = max(0, n_kv - KS); j < n_kv && !*abort; ++j)
@@ -470,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok) {
         tc_fence_after();
         if (b_0 == 0 && f_0 > 0) issue_s(0, 0);
-        if (b_1 == 0 && f_1 > 0) issue_s(1, 0);
+        if (G > 1 && b_1 == 0 && f_1 > 0) issue_s(1, 0);
         tc_commit_if(leader, bars.k_empty(0));
       }
     }
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!(ok = warp_wait(bars.v_full(it % VS), (it / VS) & 1, p.err, abort, W_VFULL))) break;
       bool k_seen = false;
 #pragma unroll
-      for (int g = 0; g < 2 && ok; ++g) {
+      for (int g = 0; g < G && ok; ++g) {
         const int bg = g ? b_1 : b_0, fg = g ? f_1 : f_0;
         if (it >= bg && it < fg) {
           if (!(ok = warp_wait(bars.p_ready(g), (it - bg) & 1, p.err, abort, W_PREADY))) break;
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       if (!FIXED && ok && i > 0) {
-        const float m_cand = fmaxf(last, s_row[(hf ^ 1) * 2 * BM]);
+        const float m_cand = fmaxf(last, s_row[(hf ^ 1) * G * BM]);
         float alpha = 1.f;
         // The first tile with a visible key, of either half, was taken at reference 0.
         if (m_ref == -INFINITY && m_cand != -INFINITY) m_ref = 0.f;
@@ -588,17 +598,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           mx = whole ? half_tile<MODE, false, true>(s_col, t, c2, cap, slope2, m_use, sum, pk)
                      : half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, pk);
         }
-        const bool again =
-            mx > HIGH_LOG2 || (m_ref == -INFINITY && mx < LOW_LOG2 && mx != -INFINITY);
-        if (rows_or(bar_id, again || !ok)) {
+        bool again = rows_or(bar_id, mx > HIGH_LOG2 || !ok);
+        if (!again && __any_sync(FULL, m_ref == -INFINITY)) {
+          // A row's first visible tile: low if both halves are. The partner, which holds
+          // the same rows and references, comes to the same answer.
+          s_row[hf * G * BM] = m_use + mx;
+          if (!(ok = rows_and(bar_id, ok))) break;
+          const float top = fmaxf(m_use + mx, s_row[(hf ^ 1) * G * BM]);
+          again = __any_sync(FULL, m_ref == -INFINITY && top < LOW_LOG2 && top != -INFINITY);
+        }
+        if (again) {
           if (!(ok = rows_and(bar_id, ok))) break;
           // The maximum first, of both halves, then P.
           sum = 0.f;
           mx = -INFINITY;
           if (!none) mx = half_tile<MODE, true, false>(s_col, t, c2, cap, slope2, 0.f, sum, pk);
-          s_row[hf * 2 * BM] = mx;
+          s_row[hf * G * BM] = mx;
           if (!(ok = rows_and(bar_id, ok))) break;
-          const float m_cand = fmaxf(mx, s_row[(hf ^ 1) * 2 * BM]);
+          const float m_cand = fmaxf(mx, s_row[(hf ^ 1) * G * BM]);
           if (!(ok = rows_and(bar_id, ok))) break;   // both have read
           float alpha = 1.f;
           if (m_cand > m_ref + RESCALE_LOG2) {
@@ -610,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!none) mx = half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, pk);
         }
         last = m_use + mx;
-        s_row[hf * 2 * BM] = last;
+        s_row[hf * G * BM] = last;
         l += sum;
         uint32_t lo16[16], hi16[16];
 #pragma unroll
@@ -630,9 +647,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const size_t out_row = static_cast<size_t>(sq.start + qpos) * p.H + h;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D + hf * (D / 2));
     if (n > 0) ok = ok && warp_wait(bars.o_full(), 0, p.err, abort, W_OFULL);
-    s_row[hf * 2 * BM] = l;   // o_full: the partner has read the last maximum
+    s_row[hf * G * BM] = l;   // o_full: the partner has read the last maximum
     ok = rows_and(bar_id, ok);
-    l += s_row[(hf ^ 1) * 2 * BM];
+    l += s_row[(hf ^ 1) * G * BM];
     if (ok) {
       tc_fence_after();
       const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
@@ -676,8 +693,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int D, int MODE>
 cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
   using C = Cfg<D>;
-  const int num_m2 = (p.max_seqlen + 2 * BM - 1) / (2 * BM);
-  const long long tiles = static_cast<long long>(num_m2) * p.H * p.B;
+  const int num_m = (p.max_seqlen + C::G * BM - 1) / (C::G * BM);
+  const long long tiles = static_cast<long long>(num_m) * p.H * p.B;
   if (tiles > INT_MAX) return cudaErrorInvalidConfiguration;
   CUtensorMap tq, tk, tv;
   if (!make_tmap_bf16_2d(&tq, p.q, p.total, static_cast<unsigned long long>(p.H) * D, 64, BM) ||
@@ -688,8 +705,8 @@ cudaError_t launch(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream
   if (e != cudaSuccess) return e;
   const int group = l2_group(4ll * p.max_seqlen * D, p.H / p.H_kv, p.H * p.B);
   const CapArgs cap = MODE >= CAPPED ? cap_args(sh.cap, p.scale) : CapArgs{};
-  shaped_fwd_kernel<D, MODE><<<static_cast<unsigned>(tiles), THREADS, C::SMEM, stream>>>(
-      tq, tk, tv, p, sh, cap, num_m2, group);
+  shaped_fwd_kernel<D, MODE><<<static_cast<unsigned>(tiles), C::THREADS, C::SMEM, stream>>>(
+      tq, tk, tv, p, sh, cap, num_m, group);
   return cudaGetLastError();
 }
 
