@@ -66,8 +66,9 @@ struct Cfg {
   static constexpr uint32_t OFF_MREF = OFF_P + PBUF * P_BYTES;  // float [NQ]: reference max
   static constexpr uint32_t OFF_ALPHA = OFF_MREF + NQ * 4;    // float [NQ]: its last move
   static constexpr uint32_t OFF_RED = OFF_ALPHA + NQ * 4;     // float [4][NQ]: per-warp max / sum
-  static constexpr uint32_t OFF_SLOPE = OFF_RED + 4 * NQ * 4; // float [NQ]: slope log2 e of a row
-  static constexpr uint32_t OFF_QPOS = OFF_SLOPE + NQ * 4;    // int [NQ]: a row's position - row 0's
+  static constexpr uint32_t OFF_SLOPE = OFF_RED + 4 * NQ * 4; // float2 [NQ]: -slope log2 e of a row,
+                                                              // its position - row 0's
+  static constexpr uint32_t OFF_QPOS = OFF_SLOPE + NQ * 8;    // int [NQ]: the same position
   static constexpr uint32_t OFF_ROWS = OFF_QPOS + NQ * 4;  // int [8][8]: paged rows per tile
   static constexpr uint32_t OFF_BAR = OFF_ROWS + 8 * 8 * 4;
   // k_full[S], k_empty[S], v_full[S], v_empty[S], q_full[QBUF], q_empty[QBUF],
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     float* mref = reinterpret_cast<float*>(smem + C::OFF_MREF);
     float* alpha_s = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
     float* red = reinterpret_cast<float*>(smem + C::OFF_RED);   // [quarter][row]
-    float* slope_s = reinterpret_cast<float*>(smem + C::OFF_SLOPE);
+    float2* bias_s = reinterpret_cast<float2*>(smem + C::OFF_SLOPE);
     int* qpos_s = reinterpret_cast<int*>(smem + C::OFF_QPOS);
     const float c2 = p.scale_log2;
     const int g = dec.g;
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (sid < NQ) {
       mref[sid] = sid < R ? 0.f : INFINITY;
       alpha_s[sid] = 1.f;
-      slope_s[sid] = (biased && sid < R) ? __ldg(sh.slopes + hk * g + sid % g) * LOG2E : 0.f;
+      bias_s[sid].x = (biased && sid < R) ? -__ldg(sh.slopes + hk * g + sid % g) * LOG2E : 0.f;
     }
     softmax_sync();
     // This thread's rows' references: the move threshold m + 8 and the
@@ -775,6 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                   : nullptr;
           const int here = (placed && sid < R && slot >= 0) ? __ldg(pos + slot) : slot;
           qpos_s[sid] = here - ((placed && s0 >= 0) ? __ldg(pos + s0) : s0);
+          bias_s[sid].y = static_cast<float>(qpos_s[sid]);
         }
         q0 = w.len - dec.q_len;
         if (placed && q0 >= 0)
@@ -804,8 +806,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (biased) {
         const float d = static_cast<float>(dist);
 #pragma unroll
-        for (int r = 0; r < NH; ++r)
-          x[r] = fmaf(-slope_s[r0 + r], fabsf(d + static_cast<float>(qpos_s[r0 + r])), x[r]);
+        for (int r = 0; r < NH; ++r) {
+          const float2 s2 = bias_s[r0 + r];
+          x[r] = fmaf(s2.x, fabsf(d + s2.y), x[r]);
+        }
       }
       // Query row r sees key `key` when key < len, causally key <= len - q_len +
       // r / g, i.e. r >= g (key - len + q_len), and within the window. A tile
@@ -1018,8 +1022,9 @@ __device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wa
 // partials, one output row per warp: LSE = ln sum_c exp(LSE_c), O = sum_c exp(LSE_c -
 // LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
 // get O = 0 and LSE = -inf here. The others: key_weights[b, hk, j] += sum_r 2^(z_rj -
-// LSE_r log2 e), four tiles of a segment per block, a warp a tile, four slots a lane.
+// LSE_r log2 e), FIN_TILES tiles of a segment per block, a warp a tile, four slots a lane.
 constexpr int FIN_THREADS = 128;
+constexpr int FIN_TILES = FIN_THREADS / 32;
 template <int D>
 __global__ void __launch_bounds__(FIN_THREADS)
     finish_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt,
@@ -1083,40 +1088,54 @@ __global__ void __launch_bounds__(FIN_THREADS)
     return;
   }
   __shared__ float lse2[64];
-  const int quads = (tiles_max + 3) / 4;
+  const int per = (tiles_max + FIN_TILES - 1) / FIN_TILES;
   const int id = static_cast<int>(blockIdx.x) - merge_blocks;
-  const int seg = id / quads;
+  const int seg = id / per, t0 = (id % per) * FIN_TILES;
   const int b = seg / p.H_kv, hk = seg % p.H_kv;
   int f, len;
   const int n = seq_tiles(seqs, b, f, len);
-  const int t = (id % quads) * 4 + warp;
-  if ((id % quads) * 4 >= n || (id % quads) * 4 + 3 < f) return;
+  if (t0 >= n || t0 + FIN_TILES <= f) return;
   wait_primary();
+  // The first rows' scores and the slots' weights are on their way while the LSEs form.
+  const int t = t0 + warp;
+  const bool on = t >= f && t < n;
+  const float* x = xs + (static_cast<size_t>(seg) * tiles_max + t) * R * BN + 4 * lane;
+  float* dst = sh.key_weights + static_cast<size_t>(seg) * sh.slots + t * BN + 4 * lane;
+  constexpr int AHEAD = 8;
+  float4 v[AHEAD];
+  float w[4] = {};
+#pragma unroll
+  for (int r = 0; r < AHEAD; ++r)
+    if (on && r < R) v[r] = *reinterpret_cast<const float4*>(x + static_cast<size_t>(r) * BN);
+  float old[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) old[k] = (on && t * BN + 4 * lane + k < len) ? dst[k] : 0.f;
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     const Pieces pc = seg_pieces(dt, seg, len);
-    const float v = pc.c0 == pc.c1 ? p.lse[static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H +
+    const float s = pc.c0 == pc.c1 ? p.lse[static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H +
                                            hk * dec.g + r % dec.g]
                                    : pieces_lse(dt, pc, b, hk, p.H_kv, R, r);
-    lse2[r] = v == -INFINITY ? 0.f : v * LOG2E;   // a row that sees nothing: its z are -inf
+    lse2[r] = s == -INFINITY ? 0.f : s * LOG2E;   // a row that sees nothing: its z are -inf
   }
   __syncthreads();
-  if (t < f || t >= n) return;
-  const float* x = xs + (static_cast<size_t>(seg) * tiles_max + t) * R * BN + 4 * lane;
-  float w[4] = {};
-#pragma unroll 4
-  for (int r = 0; r < R; ++r) {
-    const float4 v = *reinterpret_cast<const float4*>(x + static_cast<size_t>(r) * BN);
+  if (!on) return;
+  auto add = [&](const float4& s, int r) {
     const float e = lse2[r];
-    w[0] += ex2_approx(v.x - e);
-    w[1] += ex2_approx(v.y - e);
-    w[2] += ex2_approx(v.z - e);
-    w[3] += ex2_approx(v.w - e);
-  }
-  float* dst = sh.key_weights + static_cast<size_t>(seg) * sh.slots + t * BN + 4 * lane;
+    w[0] += ex2_approx(s.x - e);
+    w[1] += ex2_approx(s.y - e);
+    w[2] += ex2_approx(s.z - e);
+    w[3] += ex2_approx(s.w - e);
+  };
+#pragma unroll
+  for (int r = 0; r < AHEAD; ++r)
+    if (r < R) add(v[r], r);
+#pragma unroll 8
+  for (int r = AHEAD; r < R; ++r)
+    add(*reinterpret_cast<const float4*>(x + static_cast<size_t>(r) * BN), r);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (t * BN + 4 * lane + k < len) dst[k] += w[k];
+    if (t * BN + 4 * lane + k < len) dst[k] = old[k] + w[k];
 }
 
 struct Workspace {
@@ -1189,7 +1208,9 @@ cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShape
   const int tiles_max = (p.max_seqlen + BN - 1) / BN;
   const long long merge = (rows + FIN_THREADS / 32 - 1) / (FIN_THREADS / 32);
   const long long blocks =
-      merge + (sh.key_weights ? static_cast<long long>(p.B) * p.H_kv * ((tiles_max + 3) / 4) : 0);
+      merge + (sh.key_weights ? static_cast<long long>(p.B) * p.H_kv *
+                                   ((tiles_max + FIN_TILES - 1) / FIN_TILES)
+                             : 0);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   // Launched while the ranges still run; it waits for them before it reads.
   cudaLaunchAttribute attr = {};
