@@ -6,12 +6,14 @@
 // slots in ascending order; move_kernel copies their K and V rows into the other cache.
 //
 // The selection. Weights map to unsigned keys of the same order. The key of the n-th
-// heaviest is found digit by digit, 11 bits at a time, over key - least key: the
-// digits then spread over the bins (accumulated weights share a few exponents, so that
-// digits of the keys themselves put thousands of counts on one shared-memory address:
-// 70 us against 19 on B16 H8, 4096 to 32768 slots). Each warp then walks its own stretch
-// of slots with ballots, so that the order needs one scan over the warps' counts.
-// The keys wait in shared memory, up to 48K of them; longer rows are read again.
+// heaviest is found digit by digit, 11 bits at a time, over key - least key: the digits
+// then spread over the bins (accumulated weights share a few exponents, so that digits
+// of the keys themselves put thousands of counts on one shared-memory address: 70 us on
+// B16 H8, 4096 to 32768 slots). After the first digit the few keys that share it are
+// gathered, and the rest of the search goes over them alone. What is left is bound by
+// the instructions per slot, so the passes take four slots a lane: two per 128 slots and
+// warp for the counts, and for the order one scan of packed (tie, taken) counts by
+// shuffles. The keys wait in shared memory, up to 48K of them; longer rows are read again.
 //
 // The move is bound by its bytes: 16 of a K and a V row per thread, grid-stride.
 #include <math.h>
@@ -29,6 +31,7 @@ constexpr int WARPS = SELECT_THREADS / 32;
 constexpr int DIGIT = 11;
 constexpr int BINS = 1 << DIGIT;
 constexpr int KEYS_MAX = 48 * 1024;   // keys held in shared memory
+constexpr int LIST_MAX = 2048;        // keys gathered after a digit
 constexpr int MOVE_THREADS = 256;
 enum : unsigned { BAD_CACHE_LEN = 0xA0F01, BAD_PAGE = 0xA0F02 };
 
@@ -56,13 +59,18 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
   return v + before;
 }
 
-__global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs a, int held) {
-  extern __shared__ unsigned s_key[];   // ``held`` keys
+// Key of a slot that stays in any case: above every weight's.
+constexpr unsigned STAYS = 0xffffffffu;
+
+template <bool HELD>
+__global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) unsigned s_key[];   // HELD: the keys, to a multiple of 128
   __shared__ int hist[BINS];
+  __shared__ unsigned list[LIST_MAX];
   __shared__ int part[WARPS], part2[WARPS];
   __shared__ unsigned s_lo[WARPS], s_hi[WARPS];
   __shared__ unsigned s_digit;
-  __shared__ int s_need;
+  __shared__ int s_need, s_count, s_listed;
   const int hk = blockIdx.x % a.H_kv, b = blockIdx.x / a.H_kv, tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -77,18 +85,47 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs 
   const int old = len - min(a.recent, n);  // slots [old, len) stay in any case
   const int want = n - (len - old);        // to take of the first ``old``
   if (tid == 0 && hk == 0) a.seqlens_out[b] = n;
-  auto key = [&](int j) { return j < held ? s_key[j] : weight_key(w[j]); };
-  const bool choose = want > 0 && want < old;
-  unsigned limit = 0;   // key of the last one taken
-  int ties = 0;         // how many with that key are taken
-  if (choose) {
-    unsigned lo = 0xffffffffu, hi = 0u;
-    for (int j = tid; j < old; j += SELECT_THREADS) {
-      const unsigned k = weight_key(w[j]);
-      if (j < held) s_key[j] = k;
-      lo = min(lo, k);
-      hi = max(hi, k);
+  const bool all = want >= old, choose = want > 0 && !all;
+  // Keys of slots j .. j + 3 (j a multiple of four): STAYS in [old, len), 0 behind.
+  auto key4 = [&](int j, unsigned (&k)[4]) {
+    if (HELD) {
+      const uint4 v = *reinterpret_cast<const uint4*>(s_key + j);
+      k[0] = v.x;
+      k[1] = v.y;
+      k[2] = v.z;
+      k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        k[e] = j + e < old ? weight_key(w[j + e]) : j + e < len ? STAYS : 0u;
     }
+  };
+  unsigned lo = STAYS, hi = 0u;
+  if (HELD || choose) {
+    const int end = (len + 127) & ~127;
+    for (int base = 0; base < end; base += 8 * SELECT_THREADS) {
+      float v[8];   // eight loads on their way
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = base + k * SELECT_THREADS + tid;
+        v[k] = j < old ? w[j] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = base + k * SELECT_THREADS + tid;
+        if (j >= end) continue;
+        const unsigned u = j < old ? weight_key(v[k]) : j < len ? STAYS : 0u;
+        if (HELD) s_key[j] = u;
+        if (j < old) {
+          lo = min(lo, u);
+          hi = max(hi, u);
+        }
+      }
+    }
+  }
+  unsigned limit = STAYS - 1;   // key of the last one taken; nothing but STAYS above it
+  int ties = 0;                 // how many with that key are taken
+  if (choose) {
     lo = __reduce_min_sync(FULL, lo);
     hi = __reduce_max_sync(FULL, hi);
     if (lane == 0) {
@@ -99,21 +136,33 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs 
     lo = __reduce_min_sync(FULL, s_lo[lane]);
     hi = __reduce_max_sync(FULL, s_hi[lane]);
     // Digits of key - lo from the highest bit that differs downwards.
-    int need = want;
+    int need = want, listed = -1;   // listed: how many keys the list holds, or -1
     unsigned prefix = 0;
     int bits = 32 - __clz(hi - lo);   // undecided low bits
     while (bits > 0) {
       const int shift = max(bits - DIGIT, 0);
+      const unsigned mask = (1u << (bits - shift)) - 1u;
       for (int i = tid; i < BINS; i += SELECT_THREADS) hist[i] = 0;
       __syncthreads();
-      for (int j = tid; j < old; j += SELECT_THREADS) {
-        const unsigned k = key(j) - lo;
-        if (bits == 32 || (k >> bits) == prefix)
-          atomicAdd(&hist[(k >> shift) & ((1u << (bits - shift)) - 1u)], 1);
+      if (listed >= 0) {
+        for (int j = tid; j < listed; j += SELECT_THREADS) {
+          const unsigned k = list[j];
+          if ((k >> bits) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        }
+      } else {
+        for (int j = 4 * tid; j < old; j += 4 * SELECT_THREADS) {
+          unsigned k[4];
+          key4(j, k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned d = k[e] - lo;
+            if (j + e < old && (bits == 32 || (d >> bits) == prefix))
+              atomicAdd(&hist[(d >> shift) & mask], 1);
+          }
+        }
       }
       __syncthreads();
-      // Two bins a thread, from the top: the bin where the running count reaches
-      // ``need``.
+      // Two bins a thread, from the top: the bin where the running count reaches ``need``.
       const int d0 = BINS - 1 - 2 * tid;
       const int h0 = hist[d0], h1 = hist[d0 - 1];
       const int incl = block_scan(h0 + h1, part);
@@ -122,65 +171,97 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs 
         const bool second = need > excl + h0;
         s_digit = static_cast<unsigned>(second ? d0 - 1 : d0);
         s_need = need - excl - (second ? h0 : 0);
+        s_count = second ? h1 : h0;
+        s_listed = 0;
       }
       __syncthreads();
       prefix = (prefix << (bits - shift)) | s_digit;
       need = s_need;
       bits = shift;
+      if (bits > 0 && listed < 0 && s_count <= LIST_MAX) {
+        for (int j = 4 * tid; j < old; j += 4 * SELECT_THREADS) {
+          unsigned k[4];
+          key4(j, k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned d = k[e] - lo;
+            if (j + e < old && (d >> bits) == prefix) list[atomicAdd(&s_listed, 1)] = d;
+          }
+        }
+        __syncthreads();
+        listed = s_listed;
+      }
     }
     limit = lo + prefix;
     ties = need;
+  } else {
+    __syncthreads();   // the keys
   }
-  // Each warp's stretch of slots: how many are above the limit or stay anyway, and how
-  // many sit on it.
-  const int per = ((len + WARPS - 1) / WARPS + 31) & ~31;
-  const int j0 = warp * per, j1 = min(len, j0 + per);
-  auto sort_of = [&](int j, bool& above, bool& tie) {
-    above = tie = false;
-    if (j >= j1) return;
-    if (j >= old || want >= old) {
-      above = true;
-    } else if (choose) {
-      const unsigned k = key(j);
-      above = k > limit;
-      tie = k == limit;
+  // Each warp's stretch of slots, four a lane: how many are above the limit or stay
+  // anyway, and how many sit on it, packed (ties above bit 16; a stretch of a warp holds
+  // fewer than 2^16 slots at a time).
+  const int per = ((len + WARPS - 1) / WARPS + 127) & ~127;
+  const int j0 = min(len, warp * per), j1 = min(len, j0 + per);
+  auto sorts = [&](int j, unsigned& above, unsigned& tie) {   // bit e: slot j + e
+    above = tie = 0u;
+    unsigned k[4];
+    if (j < j1) {
+      key4(j, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e < j1 && (all || k[e] > limit)) above |= 1u << e;
+        if (j + e < j1 && !all && k[e] == limit) tie |= 1u << e;
+      }
     }
   };
   int n_above = 0, n_tie = 0;
-  for (int j = j0; j < j1; j += 32) {
-    bool above, tie;
-    sort_of(j + lane, above, tie);
-    n_above += __popc(__ballot_sync(FULL, above));
-    n_tie += __popc(__ballot_sync(FULL, tie));
+  for (int j = j0; j < j1; j += 128) {
+    unsigned above, tie;
+    sorts(j + 4 * lane, above, tie);
+    n_above += __popc(above);
+    n_tie += __popc(tie);
   }
+  n_above = __reduce_add_sync(FULL, n_above);
+  n_tie = __reduce_add_sync(FULL, n_tie);
   __syncthreads();
   if (lane == 0) {
     part[warp] = n_above;
     part2[warp] = n_tie;
   }
   __syncthreads();
-  // Ties before this warp, and places taken before it.
-  const int tie_all = part2[lane], above_all = part[lane];
-  const int tie_before = __reduce_add_sync(FULL, lane < warp ? tie_all : 0);
-  int at = __reduce_add_sync(FULL, lane < warp ? above_all : 0) + min(tie_before, ties);
-  int rank = tie_before;
-  const unsigned below = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    bool above, tie;
-    sort_of(j + lane, above, tie);
-    const unsigned t = __ballot_sync(FULL, tie);
-    const bool keep = above || (tie && rank + __popc(t & below) < ties);
-    const unsigned k = __ballot_sync(FULL, keep);
-    if (keep) {
-      const int to = at + __popc(k & below);
-      const int s = j + lane;
-      a.src[seg * a.keep + to] = s;
-      a.weights_out[seg * a.out_slots + to] = w[s];
-      a.positions_out[seg * a.out_slots + to] =
-          a.key_positions ? a.key_positions[seg * a.slots + s] : s;
+  // Ties and places before this warp.
+  int rank = __reduce_add_sync(FULL, lane < warp ? part2[lane] : 0);
+  int taken = __reduce_add_sync(FULL, lane < warp ? part[lane] : 0);
+  for (int j = j0; j < j1; j += 128) {
+    unsigned above, tie;
+    const int s = j + 4 * lane;
+    sorts(s, above, tie);
+    // Inclusive counts over the lanes: ties in the high half, above in the low.
+    const int mine = (__popc(tie) << 16) | __popc(above);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += u;
     }
-    rank += __popc(t);
-    at += __popc(k);
+    const int sum = __shfl_sync(FULL, incl, 31);
+    int r = rank + ((incl - mine) >> 16), t = taken + ((incl - mine) & 0xffff);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool is_tie = (tie >> e) & 1u, is_above = (above >> e) & 1u;
+      if (is_above || (is_tie && r < ties)) {
+        const int to = t + min(r, ties);
+        if (to >= n) break;
+        a.src[seg * a.keep + to] = s + e;
+        a.weights_out[seg * a.out_slots + to] = w[s + e];
+        a.positions_out[seg * a.out_slots + to] =
+            a.key_positions ? a.key_positions[seg * a.slots + s + e] : s + e;
+      }
+      r += is_tie;
+      t += is_above;
+    }
+    rank += sum >> 16;
+    taken += sum & 0xffff;
   }
   for (long long i = n + tid; i < a.out_slots; i += SELECT_THREADS) {
     a.weights_out[seg * a.out_slots + i] = 0.f;
@@ -216,10 +297,16 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  const int held = std::min(a.max_len, KEYS_MAX);
-  const cudaError_t e = allow_smem<select_kernel>(KEYS_MAX * 4);
+  const int keys = (a.max_len + 127) & ~127;
+  if (keys <= KEYS_MAX) {
+    const cudaError_t e = allow_smem<select_kernel<true>>(KEYS_MAX * 4);
+    if (e != cudaSuccess) return e;
+    select_kernel<true><<<a.B * a.H_kv, SELECT_THREADS, keys * sizeof(unsigned), stream>>>(a);
+  } else {
+    select_kernel<false><<<a.B * a.H_kv, SELECT_THREADS, 0, stream>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  select_kernel<<<a.B * a.H_kv, SELECT_THREADS, held * sizeof(unsigned), stream>>>(a, held);
   const long long n = static_cast<long long>(a.B) * a.keep * a.H_kv * (a.D / 8);
   // Launched while the selection still runs; it waits for it before it reads.
   cudaLaunchAttribute attr = {};

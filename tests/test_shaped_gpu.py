@@ -409,6 +409,21 @@ def test_evict_weights_with_ties_and_oddities(kind):
         run_evict(4, [2000, 199, 1501, 0, 300], 2, 64, keep, recent, weights=weights)
 
 
+@pytest.mark.parametrize("kind", ["random", "few"])
+def test_evict_more_slots_than_shared_memory_holds(kind):
+    w = (lambda rng, s: rng.integers(0, 5, s).astype(np.float32)) if kind == "few" else None
+    run_evict(21, [60001, 49152, 50000, 7], 1, 16, 9000, 100, weights=w)
+
+
+@pytest.mark.parametrize("keep", [1, 2047, 2048, 2049, 4000, 8191])
+def test_evict_at_the_size_of_the_gathered_list(keep):
+    # Two values only, or all of one binade: more keys share a digit than the list holds.
+    run_evict(22, [8192, 8191], 2, 8, keep, 0,
+              weights=lambda rng, s: 1 + rng.integers(0, 2, s).astype(np.float32) * 2.0 ** -23)
+    run_evict(23, [8192, 5000], 1, 8, keep, 1,
+              weights=lambda rng, s: (1 + rng.random(s) / 1024).astype(np.float32))
+
+
 def test_evict_positions_and_room_for_new_tokens():
     run_evict(8, [700, 30], 2, 128, 100, 10, positions=True, out_slots=160)
 
