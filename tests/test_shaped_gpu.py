@@ -463,3 +463,253 @@ def test_bad_lengths_and_pages_are_reported_not_read():
         fa.evict(k, v, n, w, keep=128, recent=0, max_seqlen_k=128, block_table=table, page_size=64)
         assert fa.check_device_error()[0] != 0
     clean()
+
+
+# ------------------------------------------------- together, streams, graphs ---
+
+def test_prefill_decode_evict_decode():
+    # A cache that is filled, read with its weights added up, thinned out and read on.
+    n, H, H_kv, D, cap, scale, window = 700, 8, 2, 128, 25.0, 128 ** -0.5, 500
+    g = torch.Generator().manual_seed(12)
+    new = 3
+    q, k, v = (torch.randn((n + new, h, D), generator=g).bfloat16() * 2 for h in (H, H_kv, H_kv))
+    slopes = torch.tensor([0.02 * 0.8 ** h for h in range(H)])
+    begin = np.maximum(0, np.arange(n) - window + 1).astype(np.int32)
+    up = lambda t: t.cuda()
+    shape = dict(softcap=cap, alibi_slopes=up(slopes))
+    # prefill
+    o, lse = fa.fwd(up(q[:n])[None], up(k[:n])[None], up(v[:n])[None], causal=True,
+                    key_begin=up(torch.from_numpy(begin))[None], **shape)
+    r = osh.forward(q[:n], k[:n], v[:n], [0, n], True, scale, cap, slopes, begin)
+    e = score_error(q, k, scale, cap, slopes, n + new, "bf16")
+    inside("prefill O", f64(o)[0], r.o, (HALF + 2 * e) * r.o_abs + HALF * np.abs(r.o))
+    # the last 8 tokens again as a decode step: the weights they give to the cache
+    room = 256
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    w = torch.zeros(1, H_kv, n, device="cuda")
+    o8, _ = fa.decode(up(q[n - 8:n]), up(k[:n]), up(v[:n]), lens, q_len=8, max_seqlen_k=n,
+                      window=window, key_weights=w, **shape)
+    inside("decode O", f64(o8), r.o[-8:], (HALF + 2 * e) * r.o_abs[-8:] + HALF * np.abs(r.o[-8:]))
+    # keep 200 of 700, room for new tokens
+    k2, v2, n2, w2, pos = fa.evict(up(k[:n]), up(v[:n]), lens, w, keep=200, recent=32,
+                                   max_seqlen_k=n, out_slots=room)
+    assert n2.tolist() == [200]
+    # three more tokens, one at a time, in slots 200 .. with positions 700 ..
+    held = [osh.kept_slots(w[0, h].cpu().numpy(), n, 200, 32) for h in range(H_kv)]
+    w_ref = np.zeros((H_kv, room))
+    for h in range(H_kv):
+        w_ref[h, :200] = w[0, h].cpu().numpy()[held[h]]
+    for t in range(new):
+        s = 200 + t
+        k2[s], v2[s] = up(k[n + t]), up(v[n + t])
+        pos[:, :, s] = n + t
+        o1, _ = fa.decode(up(q[n + t:n + t + 1]), k2, v2, n2 + t + 1, q_len=1, max_seqlen_k=room,
+                          window=window, key_positions=pos, key_weights=w2, **shape)
+        for h in range(H_kv):
+            at = np.concatenate([held[h], n + np.arange(t + 1)])
+            heads = slice(h * H // H_kv, (h + 1) * H // H_kv)
+            ro, _, ra, rw = osh.decode(q[n + t:n + t + 1, heads], k[at][:, h:h + 1], v[at][:, h:h + 1],
+                                       [s + 1], q_len=1, scale=scale, page_size=s + 1, cap=cap,
+                                       slopes=slopes[heads], window=window, positions=at[None, None])
+            inside("O after eviction", f64(o1)[:, heads], ro, (HALF + 2 * e) * ra + HALF * np.abs(ro))
+            w_ref[h, :s + 1] += rw[0, 0]
+    clean()
+    inside("weights after eviction", f64(w2)[0], w_ref, 2 * e * w_ref + 2.0 ** -20 * (1 + w_ref))
+
+
+def _small_state(seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    st = dict(q=rnd(1, 300, 4, 64), k=rnd(1, 300, 2, 64), v=rnd(1, 300, 2, 64), do=rnd(1, 300, 4, 64),
+              kc=rnd(2 * 400, 2, 64), vc=rnd(2 * 400, 2, 64), qd=rnd(2, 4, 64),
+              sl=torch.tensor([0.3, 0.2, 0.1, 0.05], device="cuda"),
+              b=torch.zeros(1, 300, dtype=torch.int32, device="cuda"),
+              lens=torch.tensor([400, 200], dtype=torch.int32, device="cuda"),
+              w=torch.rand(2, 2, 400, generator=g, device="cuda"))
+    st["b"][:, 150:] = 100
+    return st
+
+
+def _all_of_it(s):
+    kw = dict(causal=True, softcap=20.0, alibi_slopes=s["sl"], key_begin=s["b"])
+    o, lse = fa.fwd(s["q"], s["k"], s["v"], **kw)
+    grads = fa.bwd(s["do"], s["q"], s["k"], s["v"], o, lse, **kw)
+    w = s["w"].clone()
+    od, ld = fa.decode(s["qd"], s["kc"], s["vc"], s["lens"], q_len=1, max_seqlen_k=400, softcap=20.0,
+                       window=300, key_weights=w)
+    return (o, lse, *grads, od, ld, w) + fa.evict(s["kc"], s["vc"], s["lens"], w, keep=100, recent=7,
+                                                  max_seqlen_k=400)
+
+
+def _agree(a, b, exact=True):
+    for i, (x, y) in enumerate(zip(a, b)):
+        if exact and i != 2:   # dQ: reproducible to rounding
+            assert torch.equal(x, y), i
+        else:
+            assert torch.allclose(x.float(), y.float(), rtol=2 ** -6, atol=2 ** -9), i
+
+
+def test_same_inputs_same_bits():
+    s = _small_state(1)
+    _agree(_all_of_it(s), _all_of_it(s))
+    clean()
+
+
+def test_on_another_stream():
+    ref = _all_of_it(_small_state(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        busy = torch.randn(3000, 3000, device="cuda") @ torch.randn(3000, 3000, device="cuda")
+        got = _all_of_it(_small_state(2))
+    side.synchronize()
+    assert busy.isfinite().all()
+    _agree(got, ref)
+    clean()
+
+
+def test_two_streams_at_once():
+    states = [_small_state(3), _small_state(4)]
+    refs = [_all_of_it(s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = _all_of_it(states[i])
+    torch.cuda.synchronize()
+    for g, r in zip(got, refs):
+        _agree(g, r)
+    clean()
+
+
+def test_captured_and_replayed_with_new_inputs():
+    s = _small_state(5)
+    _all_of_it(s)   # the first call of each kernel on a device is made outside a capture
+    graphs, outs = [], []
+    for _ in range(2):   # two graphs of one memory pool
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=graphs[0].pool() if graphs else None):
+            outs.append(_all_of_it(s))
+        graphs.append(g)
+    for seed in (6, 7):
+        new = _small_state(seed)
+        for n in s:
+            s[n].copy_(new[n])
+        ref = [x.clone() for x in _all_of_it(new)]
+        for g, o in zip(graphs, outs):
+            g.replay()
+            torch.cuda.synchronize()
+            _agree(o, ref)
+    clean()
+
+
+def test_debug_build_runs_the_shaped_kernels():
+    from exact_io_aware_tmem_b200 import attention, build
+    build.build(debug=True)
+    s = _small_state(8)
+    ref = _all_of_it(s)
+    with attention.debug_build():
+        got = _all_of_it(s)
+        clean()
+    _agree(got, ref)
+
+
+# ------------------------------------------------------------- far and empty ---
+
+def test_pages_before_the_window_may_be_gone():
+    # Their block-table entries are invalid and the rows they had hold NaN.
+    lengths, window, page = [1000, 300, 90], 130, 64
+    c = decode_case(77, dtype="bf16", lengths=lengths, q_len=2, H=4, H_kv=2, D=128, page_size=page)
+    ro, rl, ra, rw = osh.decode(c.q, c.k_cache, c.v_cache, lengths, q_len=2, scale=128 ** -0.5,
+                                page_size=page, block_table=c.block_table, window=window)
+    for b, n in enumerate(lengths):
+        for i in range(max(0, n - window - 1) // page):
+            blk = int(c.block_table[b, i])
+            c.k_cache[blk * page:(blk + 1) * page] = float("nan")
+            c.v_cache[blk * page:(blk + 1) * page] = float("nan")
+            c.block_table[b, i] = -1
+    w = torch.zeros(3, 2, 1000, device="cuda")
+    o, lse = fa.decode(c.q.cuda(), c.k_cache.cuda(), c.v_cache.cuda(), c.cache_seqlens.cuda(), q_len=2,
+                       max_seqlen_k=1000, block_table=c.block_table.cuda(), page_size=page,
+                       window=window, key_weights=w)
+    clean()
+    inside("O", f64(o), ro, (HALF + 4e-4) * ra + HALF * np.abs(ro))
+    inside("LSE", f64(lse), rl, 2e-4)
+    inside("weights", f64(w), rw, 4e-4 * rw)
+
+
+def test_cache_rows_past_2_31_elements():
+    # 2.2 million rows of 8 heads of 128: element offsets pass 2^31, byte offsets 2^32.
+    rows, H_kv, D, page, n = 2_200_064, 8, 128, 64, 500
+    k, v = (torch.empty(rows, H_kv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pages = torch.tensor([[34375, 3, 34370, 34000, 20000, 17, 34373, 33333]], dtype=torch.int32)
+    at = osh.cache_rows(0, n, page, pages)
+    assert at.max() < rows
+    g = torch.Generator().manual_seed(1)
+    kk, vv = (torch.randn((n, H_kv, D), generator=g).bfloat16() for _ in range(2))
+    idx = torch.from_numpy(at).cuda()
+    k[idx], v[idx] = kk.cuda(), vv.cuda()
+    q = torch.randn((1, 8, D), generator=g).bfloat16()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    w = torch.zeros(1, H_kv, n, device="cuda")
+    o, lse = fa.decode(q.cuda(), k, v, lens, q_len=1, max_seqlen_k=n, block_table=pages.cuda(),
+                       page_size=page, softcap=30.0, key_weights=w)
+    ro, rl, ra, rw = osh.decode(q, kk, vv, [n], q_len=1, scale=D ** -0.5, page_size=n, cap=30.0)
+    inside("O", f64(o), ro, (HALF + 4e-4) * ra + HALF * np.abs(ro))
+    inside("weights", f64(w), rw, 4e-4 * rw)
+    out = torch.tensor([[34374, 2]], dtype=torch.int32, device="cuda")
+    _, _, n2, _, pos = fa.evict(k, v, lens, w, keep=100, recent=4, max_seqlen_k=n,
+                                block_table=pages.cuda(), page_size=page, k_out=k, v_out=v,
+                                out_block_table=out, out_page_size=page)
+    clean()
+    i = torch.arange(100)
+    to = out[0].cpu().long()[i // page] * page + i % page
+    for h in range(H_kv):
+        s = pos[0, h].long().cpu()
+        assert torch.equal(k[to.cuda(), h].cpu(), kk[s, h]) and torch.equal(v[to.cuda(), h].cpu(), vv[s, h])
+
+
+def test_tensors_past_2_31_elements():
+    # 270 thousand tokens of 64 heads of 128; each sees its last 40 keys.
+    N, H, D, window = 270_000, 64, 128, 40
+    g = torch.Generator("cuda").manual_seed(2)
+    q = torch.randn((1, N, H, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn((1, N, 1, D), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    begin = (torch.arange(N, device="cuda") - window + 1).clamp(min=0).int()[None]
+    kw = dict(causal=True, softcap=30.0, key_begin=begin)
+    o, lse = fa.fwd(q, k, v, **kw)
+    dq, dk, dv = fa.bwd(q, q, k, v, o, lse, **kw)
+    clean()
+    m = 300   # the last tokens, from those whose keys lie among them on
+    tail = lambda t: t[0, N - m:].cpu()
+    qq, kk, vv = tail(q)[:, H - 2:], tail(k), tail(v)
+    b = np.maximum(0, np.arange(m) - window + 1)
+    r = osh.forward(qq, kk, vv, [0, m], True, D ** -0.5, 30.0, None, b)
+    e = score_error(qq, kk, D ** -0.5, 30.0, None, m, "bf16")
+    s = slice(window, m)
+    inside("O", f64(tail(o)[:, H - 2:])[s], r.o[s], ((HALF + 2 * e) * r.o_abs + HALF * np.abs(r.o))[s])
+    d = osh.backward(qq, kk, vv, qq, [0, m], True, D ** -0.5, 30.0, None, b)
+    tol = (2 * HALF + 4 * e) * d.dq_abs + (HALF + 2 * e) * d.dq_del + HALF * np.abs(d.dq) + \
+        2.0 ** -20 * d.dq_raw + 2.0 ** -39 * d.dq_one
+    inside("dQ", f64(tail(dq)[:, H - 2:])[s], d.dq[s], tol[s])
+    assert torch.isfinite(dk).all() and torch.isfinite(dv).all()
+
+
+def test_nothing_to_do():
+    e = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    o, lse = fa.fwd(e(2, 0, 4, 64), e(2, 0, 2, 64), e(2, 0, 2, 64), softcap=30.0)
+    assert o.shape == (2, 0, 4, 64) and lse.shape == (2, 4, 0)
+    i32 = torch.int32
+    w = torch.rand(2, 2, 5, device="cuda")
+    w0 = w.clone()
+    od, ld = fa.decode(e(2, 4, 64) + 1, e(10, 2, 64), e(10, 2, 64), e(2, dt=i32), q_len=1,
+                       max_seqlen_k=0, page_size=5, softcap=30.0, key_weights=w)
+    assert (od == 0).all() and torch.isneginf(ld).all() and torch.equal(w, w0)
+    k2, _, n, w2, pos = fa.evict(e(10, 2, 64), e(10, 2, 64), e(2, dt=i32), w, keep=3, max_seqlen_k=0,
+                                 page_size=5)
+    assert (n == 0).all() and (w2 == 0).all() and (pos == -1).all() and (k2 == 0).all()
+    b, en = fa.key_ranges(0, B=3)
+    assert b.shape == (3, 0)
+    clean()
