@@ -116,6 +116,8 @@ cudaError_t launch_shaped_fwd_f32(const AttnParams& p, const ShapeArgs& sh, cuda
 cudaError_t launch_shaped_bwd_f32(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_fwd.cu).
 cudaError_t launch_shaped_fwd(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
+// bf16: p.delta = D_i, and zeroes in p.dq_accum (shaped_delta.cu).
+cudaError_t launch_shaped_delta(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_bwd.cu): p.delta and p.dq_accum as for the fused
 // backward, ``tiles`` shaped_bwd_tiles_bytes() of scratch.
 size_t shaped_bwd_tiles_bytes(long long total, int B);

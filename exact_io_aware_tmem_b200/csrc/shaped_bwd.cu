@@ -33,7 +33,6 @@
 
 #include <algorithm>
 
-#include "../../include/fa.h"
 #include "ex2_fma.cuh"
 #include "score_cap.cuh"
 #include "shaped.h"
@@ -810,7 +809,7 @@ size_t shaped_bwd_tiles_bytes(long long total, int B) {
 
 cudaError_t launch_shaped_bwd(const AttnParams& p, const ShapeArgs& sh, void* tiles,
                               cudaStream_t stream) {
-  cudaError_t e = launch_bwd_bf16(p, stream, FA_BWD_PHASE_PREPROCESS);
+  cudaError_t e = launch_shaped_delta(p, sh, stream);
   if (e != cudaSuccess) return e;
   int2* t = static_cast<int2*>(tiles);
   e = p.D == 64 ? sbwd::launch_d<64>(p, sh, t, stream) : sbwd::launch_d<128>(p, sh, t, stream);
