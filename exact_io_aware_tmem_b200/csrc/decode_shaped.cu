@@ -8,19 +8,25 @@
 //     O^T += V_j^T P^T  (M = 128, N = NQ, K = 128 keys);
 // segments cut by a range boundary leave partials that a second kernel joins.
 //
-// What the shape adds. A thread owns one key and NQ / 2 of the rows, so the cap
-// (tanh by exponential and reciprocal), the bias (slope x distance of two
-// positions) and the window are a few instructions on a few scores, hidden
-// behind the cache's stream. A segment's tiles are walked from its end: with a bias
-// the newest keys hold the maximum, and the reference of the softmax then hardly
-// moves (each move is two barriers and a pass over O^T). With a window the units are the tiles from the
-// first one a query sees: the others are never read.
+// What the shape adds. A thread owns one key and NH of the rows, so the cap (tanh by
+// exponential and reciprocal), the bias (slope x distance of two positions) and the
+// window are a few instructions on a few scores. What a tile costs is then the latency
+// of the chain from its scores to its P: at NQ = 16 two threads share a key, beyond four
+// do, in groups of 128 threads that own their rows and never wait for one another (16
+// sequences, 32 rows a kv head, 4096 keys each: 98 us with two threads a key and one
+// barrier for all, 89 so). A segment's tiles are walked from its end: with a bias the
+// newest keys hold the maximum, and the reference of the softmax then hardly moves (each
+// move is two barriers and a pass over O^T). With a window the units are the tiles from
+// the first one a query sees: the others are never read.
 //
 // The weights. A slot's weight needs the row's final LSE, which no CTA has while
-// it walks. Each tile's shaped scores (fp32, R x 128) go to the workspace, R x 4
-// bytes a key beside the 4 D bytes of K and V (3 % at R = 4, D = 128), and a
-// third kernel forms sum_r 2^(z_r - LSE_r) per slot from them: no second pass
-// over K, no atomics, a fixed order.
+// it walks. Each tile's shaped scores (fp32, R x 128) go to the workspace, 4 R
+// bytes a key beside the 4 D bytes of K and V (3 % at R = 4, D = 128; 25 % at R = 32),
+// and the second kernel forms sum_r 2^(z_r - LSE_r) per slot from them: no second pass
+// over K, no atomics, a fixed order. K and V are read once, so their tiles are loaded to
+// leave L2 first, and the scores are still there when they are read back (the case above
+// 89 -> 84 us; 16 sequences of up to 32768 keys in pages of 64, four rows, 205 -> 200 us,
+// 1.14 GB: 5.7 TB/s).
 //
 // D = 64: the products keep M = 128 for V^T; its second 64 rows are whatever
 // lies behind the tile in shared memory (the next V stage or the first K stage,
@@ -38,10 +44,6 @@ namespace sdec {
 
 constexpr int BN = 128;                   // keys per tile
 constexpr int STAGES = 3;
-constexpr int SOFTMAX_THREADS = 256;
-constexpr int THREADS = SOFTMAX_THREADS + 64;
-constexpr int WARP_TMA = 8;
-constexpr int WARP_MMA = 9;
 constexpr uint32_t KV_SPAN = BN * 128;    // one column block of a K / V tile
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.f;
@@ -54,6 +56,13 @@ struct Cfg {
   static constexpr int CHUNKS = D / 64;             // 128-byte column blocks of a bf16 row
   static constexpr uint32_t TILE = BN * D * 2;      // K / V tile
   static_assert(NQ == 16 || NQ == 32 || NQ == 64, "query columns");
+  // Threads a key, each with NH of the query columns.
+  static constexpr int SPLIT = NQ == 16 ? 2 : 4;
+  static constexpr int NH = NQ / SPLIT;
+  static constexpr int SOFTMAX_THREADS = SPLIT * BN;
+  static constexpr int THREADS = SOFTMAX_THREADS + 64;
+  static constexpr int WARP_TMA = SOFTMAX_THREADS / 32;
+  static constexpr int WARP_MMA = WARP_TMA + 1;
   static constexpr int QBUF = NQ <= 32 ? 2 : 1;     // Q buffers
   static constexpr int PBUF = NQ <= 32 ? 2 : 1;     // P buffers
   static constexpr uint32_t SPAN = NQ * 128;        // one column block of a Q or P tile
@@ -120,6 +129,22 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const D
   return __all_sync(FULL, ok);
 }
 
+// For tiles of K and V, which are read once: they leave L2 before the scores.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int x, int y, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
+      : "memory");
+}
+
 // Non-blocking test of a phase, agreed by the whole warp.
 __device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -133,34 +158,37 @@ __device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
   return __all_sync(FULL, done != 0);
 }
 
-// The eight softmax warps (256 threads) meet at named barrier 1. The AND
-// form also tells every thread whether all of them are still on track, so
-// that a failed wait in one warp ends the loop of all eight at the same
-// barrier; the OR form gathers a vote.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The four warps of a row group (128 threads: the keys of a tile) meet at named
+// barrier `bar`; the groups share no row and do not wait for one another. The AND form
+// also tells every thread whether all of them are still on track, so that a failed
+// wait in one warp ends the loop of all four at the same barrier; the OR form
+// gathers a vote.
+__device__ __forceinline__ void group_sync(int bar) {
+  asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+}
 
-__device__ __forceinline__ bool softmax_sync_and(bool ok) {
+__device__ __forceinline__ bool group_sync_and(int bar, bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 256, p;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"(ok ? 1u : 0u)
+      : "r"(ok ? 1u : 0u), "r"(bar)
       : "memory");
   return all != 0;
 }
 
-__device__ __forceinline__ bool softmax_sync_or(bool v) {
+__device__ __forceinline__ bool group_sync_or(int bar, bool v) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 256, p;\n\t"
+      "bar.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"(v ? 1u : 0u)
+      : "r"(v ? 1u : 0u), "r"(bar)
       : "memory");
   return any != 0;
 }
@@ -282,7 +310,7 @@ struct Walk {
 };
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
     decode_shaped_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p,
@@ -321,10 +349,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.s_full(i), 1);
-      mbar_init(bars.s_free(i), SOFTMAX_THREADS);
+      mbar_init(bars.s_free(i), C::SOFTMAX_THREADS);
     }
     for (int i = 0; i < C::PBUF; ++i) {
-      mbar_init(bars.p_ready(i), SOFTMAX_THREADS);
+      mbar_init(bars.p_ready(i), C::SOFTMAX_THREADS);
       mbar_init(bars.pv_done(i), 1);
     }
     mbar_init(bars.v_land(), 1);
@@ -334,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int groups = dt.ctas / p.H_kv;
   const int grp = blockIdx.x / p.H_kv;
   const int hk = blockIdx.x % p.H_kv;
-  if (warp == WARP_TMA) {
+  if (warp == C::WARP_TMA) {
     // This CTA's range [u0, u1) of the U = sum_b n_b units, and the tile at
     // u0: a scan of the lengths, 32 sequences per step.
     long long tot = 0;
@@ -391,13 +419,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       range[1] = u1;
     }
   }
-  if (warp == WARP_MMA) {
+  if (warp == C::WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
   // Q rows R .. NQ - 1 are never loaded: zero, so that the score columns of
   // the rows past R are exactly 0 and need no mask.
-  for (int k = threadIdx.x; k < C::QBUF * CHUNKS * (NQ - R) * 8; k += THREADS) {
+  for (int k = threadIdx.x; k < C::QBUF * CHUNKS * (NQ - R) * 8; k += C::THREADS) {
     const int unit = k % 8, row = R + (k / 8) % (NQ - R), blk = k / (8 * (NQ - R));
     *reinterpret_cast<uint4*>(smem + C::OFF_Q + blk * C::SPAN + row * 128 + unit * 16) =
         make_uint4(0, 0, 0, 0);
@@ -421,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (w0.u0 < w0.u1) w0.n = seq_tiles(seqs, w0.b, w0.f, w0.len);
   auto advance = [&](Walk& w) { w.next(seqs); };
 
-  if (warp == WARP_TMA) {
+  if (warp == C::WARP_TMA) {
     // ------------------------------------------------------------ producer ---
     // The whole warp runs the loop; lane 0 issues Q and contiguous tiles,
     // lane u box u of a paged tile. Three independent streams: Q per piece
@@ -434,6 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int box = paged ? min(dec.page, BN) : BN;   // rows per TMA box
     const int n_box = BN / box;                       // boxes (pages) per tile
     const int tpp = paged ? max(dec.page / BN, 1) : 1;   // tiles per page, pages >= 128 rows
+    const uint64_t pol = read_once_policy();
     int* rows_s = reinterpret_cast<int*>(smem + C::OFF_ROWS);
     struct PageBatch {
       int base, cur, nxt;
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int row = w.b * dec.page + w.t * BN;
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c)
-            tma_load_2d(dst + c * KV_SPAN, map, bar, hk * D + c * 64, row);
+            tma_load_once(dst + c * KV_SPAN, map, bar, hk * D + c * 64, row, pol);
         }
       } else {
         int row;
@@ -495,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane < n_box) {
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c)
-            tma_load_2d(dst + c * KV_SPAN + lane * box * 128, map, bar, hk * D + c * 64, row);
+            tma_load_once(dst + c * KV_SPAN + lane * box * 128, map, bar, hk * D + c * 64, row, pol);
         }
       }
     };
@@ -606,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait(bars.q_empty(j % C::QBUF), (j / C::QBUF) & 1, p.err, abort, W_QEMPTY))
           break;
     }
-  } else if (warp == WARP_MMA) {
+  } else if (warp == C::WARP_MMA) {
     // ---------------------------------------------------------- MMA issuer ---
     // The whole warp runs the loop; one elected lane issues and commits.
     const uint32_t leader = elect_one();
@@ -691,11 +720,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------- softmax ---
     // Warp w owns TMEM lanes 32 (w % 4) .. +31 (keys of a tile; rows of O^T
     // at the end of a piece) and query rows [NH (w / 4), NH (w / 4 + 1)).
-    constexpr int NH = NQ / 2;
-    const int sid = threadIdx.x;                 // 0 .. 255
+    constexpr int NH = C::NH;
+    const int bar = 1 + (warp >> 2);             // the group's barrier
     const int quarter = warp & 3;
     const int kt = quarter * 32 + lane;          // key of the tile / row d of O^T
     const int r0 = (warp >> 2) * NH;             // this thread's first query row
+    const int own = r0 + kt;                     // the row that thread kt < NH keeps for its group
+    const bool keeper = kt < NH && own < R;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     float* mref = reinterpret_cast<float*>(smem + C::OFF_MREF);
     float* alpha_s = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
@@ -718,12 +749,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Rows past R: scores 0 (zero Q rows) or -inf (masked), reference +inf
     // and no move, so their P is 2^-inf = 0 and the per-row loops below run
     // over all of this thread's rows without a branch.
-    if (sid < NQ) {
-      mref[sid] = sid < R ? 0.f : INFINITY;
-      alpha_s[sid] = 1.f;
-      bias_s[sid].x = (biased && sid < R) ? -__ldg(sh.slopes + hk * g + sid % g) * LOG2E : 0.f;
+    if (kt < NH) {
+      mref[own] = keeper ? 0.f : INFINITY;
+      alpha_s[own] = 1.f;
+      bias_s[own].x = (biased && keeper) ? -__ldg(sh.slopes + hk * g + own % g) * LOG2E : 0.f;
     }
-    softmax_sync();
+    group_sync(bar);
     // This thread's rows' references: the move threshold m + 8 and the
     // exponent offset (0 while a row has seen no key, m = -inf), kept in
     // registers up to 16 rows a thread, read from shared memory beyond.
@@ -768,20 +799,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r) l[r] = 0.f;
         // The rows' positions (a token before slot 0 has its slot number).
-        if (sid < NQ) {
-          const int slot = w.len - dec.q_len + sid / g;
+        if (kt < NH) {
+          const int slot = w.len - dec.q_len + own / g;
           const int s0 = w.len - dec.q_len;
           const int* pos = placed ? sh.key_positions +
                                         (static_cast<size_t>(w.b) * p.H_kv + hk) * sh.slots
                                   : nullptr;
-          const int here = (placed && sid < R && slot >= 0) ? __ldg(pos + slot) : slot;
-          qpos_s[sid] = here - ((placed && s0 >= 0) ? __ldg(pos + s0) : s0);
-          bias_s[sid].y = static_cast<float>(qpos_s[sid]);
+          const int here = (placed && keeper && slot >= 0) ? __ldg(pos + slot) : slot;
+          qpos_s[own] = here - ((placed && s0 >= 0) ? __ldg(pos + s0) : s0);
+          bias_s[own].y = static_cast<float>(qpos_s[own]);
         }
         q0 = w.len - dec.q_len;
         if (placed && q0 >= 0)
           q0 = __ldg(sh.key_positions + (static_cast<size_t>(w.b) * p.H_kv + hk) * sh.slots + q0);
-        softmax_sync();
+        group_sync(bar);
       }
       const int key = w.t * BN + kt;
       const int kpos = (placed && key < w.len)
@@ -839,8 +870,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // Does any score move its row's reference (or has a wait failed)? The
       // rare yes takes a second barrier that tells the two apart.
-      const bool any = softmax_sync_or(ex || !ok);
-      if (any && !softmax_sync_and(ok)) break;
+      const bool any = group_sync_or(bar, ex || !ok);
+      if (any && !group_sync_and(bar, ok)) break;
       const bool move = first || any;
       bool rescale = false;
       if (move) {
@@ -855,20 +886,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) red[quarter * NQ + r0 + r] = v;
           }
         }
-        softmax_sync();
-        if (sid < R) {
-          const float tmax = fmaxf(fmaxf(red[sid], red[NQ + sid]),
-                                   fmaxf(red[2 * NQ + sid], red[3 * NQ + sid]));
-          const float mo = first ? -INFINITY : mref[sid];
+        group_sync(bar);
+        if (keeper) {
+          const float tmax = fmaxf(fmaxf(red[own], red[NQ + own]),
+                                   fmaxf(red[2 * NQ + own], red[3 * NQ + own]));
+          const float mo = first ? -INFINITY : mref[own];
           float mn = mo, a = 1.f;
           if (tmax > mo + RESCALE_LOG2) {
             mn = tmax;
             a = (mo == -INFINITY) ? 0.f : ex2_approx(mo - tmax);
           }
-          mref[sid] = mn;
-          alpha_s[sid] = a;
+          mref[own] = mn;
+          alpha_s[own] = a;
         }
-        softmax_sync();
+        group_sync(bar);
         load_ref();
         if (!first) {
 #pragma unroll
@@ -937,7 +968,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) red[quarter * NQ + r0 + r] = v;
           }
         }
-        if (!softmax_sync_and(ok)) break;
+        if (!group_sync_and(bar, ok)) break;
         ok = warp_wait(bars.pv_done(i % C::PBUF), (i / C::PBUF) & 1, p.err, abort, W_PVDONE);
         if (ok) {
           tc_fence_after();
@@ -962,20 +993,20 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           }
-          if (sid < R) {
+          if (keeper) {
             const float lt =
-                (red[sid] + red[NQ + sid]) + (red[2 * NQ + sid] + red[3 * NQ + sid]);
+                (red[own] + red[NQ + own]) + (red[2 * NQ + own] + red[3 * NQ + own]);
             const float lse =
-                (lt > 0.f) ? (mref[sid] + __log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                (lt > 0.f) ? (mref[own] + __log2f(lt)) * 0.69314718055994531f : -INFINITY;
             if (whole) {
-              const size_t orow = static_cast<size_t>(w.b * dec.q_len + sid / g) * p.H +
-                                  hk * g + sid % g;
+              const size_t orow = static_cast<size_t>(w.b * dec.q_len + own / g) * p.H +
+                                  hk * g + own % g;
               p.lse[orow] = lse;
             } else {
-              dt.lse_part[slot + sid] = lse;
+              dt.lse_part[slot + own] = lse;
             }
           }
-          if (sid == 0) {
+          if (threadIdx.x == 0) {
             if (t0 + 1 == w.n) dt.seg_first[seg] = grp;
             if (w.t == w.f) dt.seg_last[seg] = grp;
           }
@@ -988,7 +1019,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == WARP_MMA) {
+  if (warp == C::WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -1023,13 +1054,14 @@ __device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wa
 // LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
 // get O = 0 and LSE = -inf here. The others: key_weights[b, hk, j] += sum_r 2^(z_rj -
 // LSE_r log2 e), FIN_TILES tiles of a segment per block, a warp a tile, four slots a lane.
+// `walked`: the most tiles a segment can have, from the first one that a query sees.
 constexpr int FIN_THREADS = 128;
 constexpr int FIN_TILES = FIN_THREADS / 32;
 template <int D>
 __global__ void __launch_bounds__(FIN_THREADS)
     finish_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt,
                   const DecodeShapeArgs sh, const Lens seqs, const float* __restrict__ xs,
-                  int merge_blocks, int tiles_max) {
+                  int merge_blocks, int tiles_max, int walked) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int R = dec.n_rows;
   if (static_cast<int>(blockIdx.x) < merge_blocks) {
@@ -1088,17 +1120,18 @@ __global__ void __launch_bounds__(FIN_THREADS)
     return;
   }
   __shared__ float lse2[64];
-  const int per = (tiles_max + FIN_TILES - 1) / FIN_TILES;
+  const int per = (walked + FIN_TILES - 1) / FIN_TILES;
   const int id = static_cast<int>(blockIdx.x) - merge_blocks;
-  const int seg = id / per, t0 = (id % per) * FIN_TILES;
+  const int seg = id / per;
   const int b = seg / p.H_kv, hk = seg % p.H_kv;
   int f, len;
   const int n = seq_tiles(seqs, b, f, len);
-  if (t0 >= n || t0 + FIN_TILES <= f) return;
+  const int t0 = f + (id % per) * FIN_TILES;
+  if (t0 >= n) return;
   wait_primary();
   // The first rows' scores and the slots' weights are on their way while the LSEs form.
   const int t = t0 + warp;
-  const bool on = t >= f && t < n;
+  const bool on = t < n;
   const float* x = xs + (static_cast<size_t>(seg) * tiles_max + t) * R * BN + 4 * lane;
   float* dst = sh.key_weights + static_cast<size_t>(seg) * sh.slots + t * BN + 4 * lane;
   constexpr int AHEAD = 8;
@@ -1176,7 +1209,7 @@ cudaError_t launch_nq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const cudaError_t e = allow_smem<decode_shaped_kernel<D, NQ>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const CapArgs cap = sh.cap > 0.f ? cap_args(sh.cap, p.scale) : CapArgs{};
-  decode_shaped_kernel<D, NQ><<<static_cast<unsigned>(w.t.ctas), THREADS, C::SMEM, stream>>>(
+  decode_shaped_kernel<D, NQ><<<static_cast<unsigned>(w.t.ctas), C::THREADS, C::SMEM, stream>>>(
       tq, tk, tv, p, d, w.t, sh, cap, seqs, w.xs);
   return cudaGetLastError();
 }
@@ -1206,10 +1239,12 @@ cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShape
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.H_kv * d.n_rows;
   const int tiles_max = (p.max_seqlen + BN - 1) / BN;
+  const int walked = static_cast<int>(
+      min(static_cast<long long>(tiles_max), (static_cast<long long>(seqs.reach) + BN - 1) / BN + 1));
   const long long merge = (rows + FIN_THREADS / 32 - 1) / (FIN_THREADS / 32);
   const long long blocks =
       merge + (sh.key_weights ? static_cast<long long>(p.B) * p.H_kv *
-                                   ((tiles_max + FIN_TILES - 1) / FIN_TILES)
+                                   ((walked + FIN_TILES - 1) / FIN_TILES)
                              : 0);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   // Launched while the ranges still run; it waits for them before it reads.
@@ -1223,7 +1258,7 @@ cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShape
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, finish_kernel<D>, p, d, w.t, sh, seqs,
-                            static_cast<const float*>(w.xs), static_cast<int>(merge), tiles_max);
+                            static_cast<const float*>(w.xs), static_cast<int>(merge), tiles_max, walked);
 }
 
 }  // namespace sdec
