@@ -9,7 +9,7 @@
 // segments cut by a range boundary leave partials that a second kernel joins.
 //
 // What the shape adds. A thread owns one key and NH of the rows, so the cap (tanh by
-// exponential and reciprocal), the bias (slope x distance of two positions) and the
+// a polynomial, or exponential and reciprocal), the bias (slope x distance of two positions) and the
 // window are a few instructions on a few scores. What a tile costs is then the latency
 // of the chain from its scores to its P: at NQ = 16 two threads share a key, beyond four
 // do, in groups of 128 threads that own their rows and never wait for one another (16
@@ -828,10 +828,27 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
         mbar_arrive(bars.s_free(i & 1));
       }
       float x[NH];
+      if (capped) {
+        // The polynomial while a warp's scores allow it: it keeps logits far below the cap
+        // to the precision of fp32.
+        float most = 0.f;
 #pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        const float v = __uint_as_float(s[r]);
-        x[r] = capped ? cap_exact(cap, v) : v * c2;
+        for (int r = 0; r < NH; ++r) most = fmaxf(most, fabsf(__uint_as_float(s[r])));
+        if (cap_form(cap, most) == 0) {
+#pragma unroll
+          for (int r = 0; r < NH; r += 2) {
+            const float2 sc = make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1]));
+            const float2 z = __fmul2_rn(sc, cap_poly2<0>(cap, sc));
+            x[r] = z.x;
+            x[r + 1] = z.y;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < NH; ++r) x[r] = cap_exact(cap, __uint_as_float(s[r]));
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < NH; ++r) x[r] = __uint_as_float(s[r]) * c2;
       }
       const int dist = q0 - kpos;   // of row 0; row r is qpos_s[r] further on
       if (biased) {

@@ -35,27 +35,34 @@ struct CapArgs {
   float k2;           // e^(2u) = 2^(k2 s)
 };
 
-// A form whose coefficients leave fp32's normal range, for an extreme scale / cap,
-// gets a limit of -1: nothing takes it.
+// For an extreme scale / cap the coefficients leave fp32's normal range. Too large: the
+// form gets a limit of -1 and nothing takes it. Too small, under a large cap: term i and
+// those behind it are dropped and the form ends where they would reach 2^-26 of the
+// first, |u| <= 2^(-13 / i); the exponential form, good to cap 2^-22 only, would lose
+// logits far below such a cap.
 inline CapArgs cap_args(float cap, float scale) {
   CapArgs a = {};
   const double log2e = 1.4426950408889634, c1 = static_cast<double>(scale) / cap;
   const double amp = cap * log2e;
-  auto normal = [](double x) { return fabs(x) > 1e-37 && fabs(x) < 1e37; };
-  auto fill = [&](float* to, const double* c, int n) {
-    bool ok = normal(1.0 / (amp * amp));
+  // Coefficients into `to`; returns the largest |s| for the form.
+  auto fill = [&](float* to, const double* c, int n, double end) {
     double pw = amp * c1;
+    bool ok = 1.0 / (amp * amp) < 1e37 && pw > 1e-37, drop = false;
     for (int i = 0; i < n; ++i, pw *= c1 * c1) {
-      to[i] = static_cast<float>(pw * c[i]);
-      ok = ok && normal(pw * c[i]);
+      if (!drop && fabs(pw * c[i]) < 1e-37) {
+        drop = true;
+        if (i > 0) end = fmin(end, exp2(-13.0 / i));
+      }
+      ok = ok && fabs(pw * c[i]) < 1e37;
+      to[i] = drop ? 0.f : static_cast<float>(pw * c[i]);
     }
-    return ok;
+    return ok ? static_cast<float>(fmin(end / c1, 1e18)) : -1.f;   // s^2 stays finite
   };
   a.amp = static_cast<float>(amp);
   a.inv_amp2 = static_cast<float>(1.0 / (amp * amp));
   a.k2 = static_cast<float>(2.0 * log2e * c1);
-  a.few_limit = fill(a.few, CAP_FEW_C, CAP_FEW) ? static_cast<float>(CAP_FEW_END / c1) : -1.f;
-  a.more_limit = fill(a.more, CAP_MORE_C, CAP_MORE) ? static_cast<float>(CAP_MORE_END / c1) : -1.f;
+  a.few_limit = fill(a.few, CAP_FEW_C, CAP_FEW, CAP_FEW_END);
+  a.more_limit = fill(a.more, CAP_MORE_C, CAP_MORE, CAP_MORE_END);
   return a;
 }
 

@@ -17,7 +17,10 @@ bool plain(const fa_score_shape* s) {
                           s->key_begin == nullptr && s->key_end == nullptr);
 }
 
-bool cap_ok(float cap) { return cap == 0.f || (cap > 0.f && isfinite(cap)); }
+// Bounds within which cap, scale / cap and their products stay in fp32's range.
+bool cap_ok(float cap, float scale) {
+  return cap == 0.f || (cap > 0.f && cap <= 0x1p100f && scale / cap <= 0x1p100f);
+}
 
 ShapeArgs shape_args(const fa_score_shape& s, float scale) {
   ShapeArgs a = {};
@@ -52,7 +55,7 @@ fa_status fa_fwd_shaped(const void* q, const void* k, const void* v, void* o, fl
   const fa_status st = fa::check_common(p, B, H, H_kv, N, D, dtype, causal, scale, cu_seqlens,
                                         max_seqlen, total_tokens);
   if (st != FA_OK) return st;
-  if (!fa::cap_ok(shape->softcap)) return FA_ERR_INVALID_ARG;
+  if (!fa::cap_ok(shape->softcap, p.scale)) return FA_ERR_INVALID_ARG;
   if (p.total == 0 || p.max_seqlen == 0 || B == 0) return FA_OK;
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!fa::aligned16(q) || !fa::aligned16(k) || !fa::aligned16(v) || !fa::aligned16(o))
@@ -89,7 +92,7 @@ fa_status fa_bwd_shaped(const void* q, const void* k, const void* v, const void*
   const fa_status st = fa::check_common(p, B, H, H_kv, N, D, dtype, causal, scale, cu_seqlens,
                                         max_seqlen, total_tokens);
   if (st != FA_OK) return st;
-  if (!fa::cap_ok(shape->softcap)) return FA_ERR_INVALID_ARG;
+  if (!fa::cap_ok(shape->softcap, p.scale)) return FA_ERR_INVALID_ARG;
   if (p.total == 0 || p.max_seqlen == 0 || B == 0) return FA_OK;
   if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace)
     return FA_ERR_INVALID_ARG;
@@ -156,11 +159,14 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
   AttnParams p = {};
   fa::DecodeArgs d = {};
   bool empty = false;
-  if (!fa::cap_ok(shape->softcap) || shape->window < 0) return FA_ERR_INVALID_ARG;
+  if (shape->window < 0) return FA_ERR_INVALID_ARG;
   const fa_status st = fa::check_decode(p, d, empty, q, k_cache, v_cache, o, lse, cache_seqlens,
                                         block_table, B, q_len, H, H_kv, D, page_size, max_blocks,
                                         cache_rows, max_seqlen_k, causal, scale);
-  if (st != FA_OK || empty) return st;
+  if (st != FA_OK) return st;
+  // (An empty call's scale was not resolved; any positive one will do.)
+  if (!fa::cap_ok(shape->softcap, empty ? 1.f : p.scale)) return FA_ERR_INVALID_ARG;
+  if (empty) return st;
   if (d.n_rows > 64) return FA_ERR_UNSUPPORTED;
   if ((shape->key_positions || shape->key_weights) && shape->slots < max_seqlen_k)
     return FA_ERR_INVALID_ARG;
@@ -222,6 +228,7 @@ fa_status fa_cache_evict(const void* k_cache, const void* v_cache, const int* ca
   // Rows move while others are read: the two caches may share memory only as
   // pages of one pool.
   const size_t row = static_cast<size_t>(H_kv) * D * 2;
+  if (fa::overlap(k_out, out_rows * row, v_out, out_rows * row)) return FA_ERR_INVALID_ARG;
   if (block_table == nullptr || out_block_table == nullptr) {
     const void* from[] = {k_cache, v_cache};
     const void* to[] = {k_out, v_out};

@@ -425,9 +425,9 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v, const float*
  * The pages ask for masks and padding without answering ("Flash Attention
  * self-test", section C); the cap, the bias and the ranges are this library's.
  *
- *   softcap       > 0 and finite; 0: no cap
- *   alibi_slopes  device float32 [H], or NULL: no bias. Constants: they get no
- *                 gradient.
+ *   softcap       > 0, softcap and scale / softcap at most 2^100; 0: no cap
+ *   alibi_slopes  device float32 [H], finite, or NULL: no bias. Constants: they
+ *                 get no gradient.
  *   key_begin,    device int32, one entry per token ([B, N] dense, [T] packed),
  *   key_end       counted from the start of the token's own sequence, or NULL
  *                 (0 / the sequence's length). Entries outside the sequence
@@ -457,8 +457,10 @@ size_t fa_bwd_shaped_workspace_size(long long total_tokens, int B, int H, int D,
 
 /*
  * fa_bwd_shaped - gradients of fa_fwd_shaped for the loss sum(O * dO):
- *   P = exp(z - LSE), dV = P^T dO, dZ = P * (dO V^T - D_i), D_i = dO_i . O_i,
- *   dX = dZ * (1 - tanh(x / softcap)^2), dQ = scale dX K, dK = scale dX^T Q.
+ *   P = exp(z - LSE), dP = dO V^T, dV = P^T dO, dZ = P * (dP - D_i),
+ *   dX = dZ * (1 - tanh(x / softcap)^2), dQ = scale dX K, dK = scale dX^T Q,
+ *   D_i = dO_i . O_i for fp32; for bf16 D_i = sum_j P_ij dP_ij, the same number
+ *   without the rounding of O (o is not read).
  * Arguments as for fa_bwd and the fa_fwd_shaped call that gave o and lse. For
  * bf16 dQ is reproducible to rounding only (its fp32 additions over key tiles
  * have no fixed order); dK and dV are bitwise reproducible.
@@ -556,7 +558,7 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
  *   out_slots      >= min(keep, max_seqlen_k)
  *   workspace      device, 16-byte aligned, at least
  *                  fa_cache_evict_workspace_size(B, H_kv, keep) bytes
- * The outputs must not overlap the inputs. A cache_seqlens entry outside
+ * The outputs must not overlap the inputs or each other. A cache_seqlens entry outside
  * [0, max_seqlen_k] is reported by fa_check_device_error, and that sequence is
  * left unwritten.
  */

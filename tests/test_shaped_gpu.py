@@ -8,7 +8,7 @@ score z in fp32 (the D products' sums, the cap, the base-2 exponent's rounding) 
   O    P rounded to bf16, O rounded:          (2^-8 + 2e) P|V| + 2^-8 |O|
   LSE                                         e
   dV   as O:                                  (2^-8 + 2e) P^T|dO| + 2^-8 |dV|
-  dQ   P (once more for dS) and dS rounded, D_i from the rounded O, dQ rounded:
+  dQ   P (once more for dS) and dS rounded, D_i = sum P dP in fp32, dQ rounded:
        (2^-7 + 4e) scale |dX||K| + (2^-8 + 2e) (what D_i moves) + 2^-8 |dQ|;  dK alike.
        Under a cap 1 - t^2 is formed from a t = tanh that fp32 gives to 2^-22 (a few
        steps of 2^-24, |t| <= 1), and is off by 2 t 2^-22 + 2^-24 < 2^-20 however small
@@ -187,6 +187,35 @@ def test_caps_of_every_size(D, cap):
     # std 4 and, at a scale of 2, far over 100.
     run_case(11, "bf16", [300], 2, 1, D, False, True, cap, False, "none", std=2.0)
     run_case(12, "bf16", [300], 2, 1, D, False, False, cap, False, "any", std=2.0, scale=2.0)
+
+
+@pytest.mark.parametrize("cap", [1e5, 1e8, 1e12, 2.0 ** 100])
+@pytest.mark.parametrize("D", [64, 128])
+def test_logits_far_below_a_large_cap(D, cap):
+    # tanh leaves them as they are to fp32, (x / cap)^2 / 3 < 2^-26: the bounds are those
+    # of scores without a cap, but for 2^-22 z of the polynomial.
+    n, H, scale = 300, 2, D ** -0.5
+    g = torch.Generator().manual_seed(D)
+    q, k, v, do = (torch.randn((n, H, D), generator=g).bfloat16() for _ in range(4))
+    up = [x.cuda()[None] for x in (q, k, v, do)]
+    kw = dict(causal=True, softcap=cap)
+    o, lse = fa.fwd(*up[:3], **kw)
+    dq = fa.bwd(up[3], *up[:3], o, lse, **kw)[0]
+    w = torch.zeros(1, H, n, device="cuda")
+    od, ld = fa.decode(q[-1:].cuda(), k.cuda(), v.cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+                       q_len=1, max_seqlen_k=n, softcap=cap, key_weights=w)
+    clean()
+    r = osh.forward(q, k, v, [0, n], True, scale, cap)
+    e = score_error(q, k, scale, 0.0, None, n, "bf16")
+    inside("LSE", f64(lse)[0], r.lse, e)
+    inside("O", f64(o)[0], r.o, (HALF + 2 * e) * r.o_abs + HALF * np.abs(r.o))
+    b = osh.backward(q, k, v, do, [0, n], True, scale, cap)
+    inside("dQ", f64(dq)[0], b.dq, (2 * HALF + 4 * e) * b.dq_abs + (HALF + 2 * e) * b.dq_del +
+           HALF * np.abs(b.dq) + 2.0 ** -20 * b.dq_raw + 2.0 ** -39 * b.dq_one)
+    ro, rl, ra, rw = osh.decode(q[-1:], k, v, [n], q_len=1, scale=scale, page_size=n, cap=cap)
+    inside("decode O", f64(od), ro, (HALF + 2 * e) * ra + HALF * np.abs(ro))
+    inside("decode LSE", f64(ld), rl, e)
+    inside("weights", f64(w), rw, 2 * e * rw + 2.0 ** -22 * (1 + rw))
 
 
 @pytest.mark.parametrize("D", [64, 128])

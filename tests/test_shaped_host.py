@@ -135,6 +135,14 @@ def test_bad_caps_are_refused(lib, cap):
     assert _decode(lib, _abi.DecodeShape(cap, None, 0, None, None, 0)) == _abi.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("cap,scale", [(2.0 ** 101, 1.0), (2.0 ** -101, 1.0), (1e-40, 0.0)])
+def test_caps_out_of_range_are_refused(lib, cap, scale):
+    assert _fwd(lib, _shape(softcap=cap), scale=scale) == _abi.FA_ERR_INVALID_ARG
+    assert _bwd(lib, _shape(softcap=cap), scale=scale) == _abi.FA_ERR_INVALID_ARG
+    assert _decode(lib, _abi.DecodeShape(cap, None, 0, None, None, 0),
+                   scale=scale) == _abi.FA_ERR_INVALID_ARG
+
+
 def _bwd(lib, shape, ws=256, short=0, **kw):
     a = dict(q=256, k=256, v=256, o=256, lse=256, dout=256, dq=256, dk=256, dv=256, B=1, H=2,
              H_kv=2, N=8, D=64, dtype=_abi.FA_BF16, causal=0, scale=0.0, cu=None, max_seqlen=0,
@@ -208,7 +216,8 @@ def _evict(lib, **kw):
     dict(weights=None), dict(weights_out=None), dict(v_out=4 * (1 << 30) + 8), dict(ws=None),
     dict(ws_bytes=10), dict(B=-1), dict(max_len=-1),
     dict(k_out=1 << 30), dict(v_out=(1 << 30) + 1024),          # the cache itself
-    dict(k_out=1 << 30, out_table=P16, out_page=64, out_blocks=2, out_rows=2048)])
+    dict(k_out=1 << 30, out_table=P16, out_page=64, out_blocks=2, out_rows=2048),
+    dict(k_out=4 * (1 << 30) + 1024)])                          # k_out over v_out
 def test_evict_refuses(lib, kw):
     assert _evict(lib, **kw) == _abi.FA_ERR_INVALID_ARG
 
@@ -236,3 +245,7 @@ def test_binding_refuses_side_tensors_that_do_not_fit():
         fa.evict(k, k, lens, torch.zeros(2, 2, 4), keep=2, max_seqlen_k=4)
     with pytest.raises(ValueError):
         fa.key_ranges()
+    with pytest.raises(ValueError):
+        fa.key_ranges(doc_ids=torch.zeros(1, 8, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        fa.key_ranges(8, device="cpu")
