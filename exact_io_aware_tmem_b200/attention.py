@@ -121,6 +121,13 @@ def _same(what: str, like: torch.Tensor, **tensors):
             raise ValueError(f"{name} must match {what} in shape, dtype and device and be contiguous")
 
 
+def _room(workspace: torch.Tensor, device: torch.device) -> int:
+    """Bytes of a workspace after its checks."""
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
 def _beside(q: torch.Tensor, k: torch.Tensor):
     """k differs from q in its heads only."""
     a, b = q.shape, k.shape
@@ -224,8 +231,8 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
               dk.data_ptr(), dv.data_ptr(), B, H, H_kv, N, D, dtype, int(bool(causal)),
               -1.0 if scale is None else float(scale), _ptr(cu_seqlens), max_sl, T,
-              ctypes.byref(shape), workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _stream(q.device))
+              ctypes.byref(shape), workspace.data_ptr(), _room(workspace, q.device),
+              _stream(q.device))
         return dq, dk, dv
     need = workspace_size(T, H, D, q.dtype, phases)
     if workspace is None:
@@ -265,7 +272,9 @@ def key_ranges(N: Optional[int] = None, *, B: int = 1, causal: bool = True,
             device = t.device
             break
     device = torch.device(device)
-    if device.type == "cuda" and device.index is None:
+    if device.type != "cuda":
+        raise ValueError("key_ranges runs on CUDA tensors")
+    if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     if cu_seqlens is not None:
         if max_seqlen is None:
@@ -404,7 +413,7 @@ def _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, bloc
         with torch.cuda.device(dev):
             need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, max_seqlen_k,
                                        int(key_weights is not None))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+    if need and (workspace is None or _room(workspace, dev) < need):
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
     _call("fa_decode_shaped", lib.fa_decode_shaped, dev, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), cache_seqlens.data_ptr(),
@@ -465,7 +474,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_seqlens: torch.Ten
     positions = torch.empty((B, H_kv, out_slots), dtype=torch.int32, device=dev)
     lib = _lib()
     need = lib.fa_cache_evict_workspace_size(B, H_kv, int(keep))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
+    if workspace is None or _room(workspace, dev) < need:
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
     _call("fa_cache_evict", lib.fa_cache_evict, dev, k_cache.data_ptr(), v_cache.data_ptr(),
           cache_seqlens.data_ptr(), _ptr(block_table), B, H_kv, D, int(page_size),
