@@ -14,7 +14,7 @@
 // of the chain from its scores to its P: at NQ = 16 two threads share a key, beyond four
 // do, in groups of 128 threads that own their rows and never wait for one another (16
 // sequences, 32 rows a kv head, 4096 keys each: 98 us with two threads a key and one
-// barrier for all, 89 so). A segment's tiles are walked from its end: with a bias the
+// barrier for all, 89 so; 64 rows, 4096 keys, cap and bias: 227 and 145). A segment's tiles are walked from its end: with a bias the
 // newest keys hold the maximum, and the reference of the softmax then hardly moves (each
 // move is two barriers and a pass over O^T). With a window the units are the tiles from
 // the first one a query sees: the others are never read.
@@ -757,8 +757,8 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
     group_sync(bar);
     // This thread's rows' references: the move threshold m + 8 and the
     // exponent offset (0 while a row has seen no key, m = -inf), kept in
-    // registers up to 16 rows a thread, read from shared memory beyond.
-    constexpr bool REF_REGS = NH <= 16;
+    // registers up to 8 rows a thread, read from shared memory beyond.
+    constexpr bool REF_REGS = NH <= 8;
     float mt[REF_REGS ? NH : 1], mu[REF_REGS ? NH : 1];
     auto load_ref = [&]() {
       if constexpr (REF_REGS) {
