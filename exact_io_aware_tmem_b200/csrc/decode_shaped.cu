@@ -14,10 +14,11 @@
 // of the chain from its scores to its P: at NQ = 16 two threads share a key, beyond four
 // do, in groups of 128 threads that own their rows and never wait for one another (16
 // sequences, 32 rows a kv head, 4096 keys each: 98 us with two threads a key and one
-// barrier for all, 89 so; 64 rows, 4096 keys, cap and bias: 227 and 145). A segment's tiles are walked from its end: with a bias the
-// newest keys hold the maximum, and the reference of the softmax then hardly moves (each
-// move is two barriers and a pass over O^T). With a window the units are the tiles from
-// the first one a query sees: the others are never read.
+// barrier for all, 89 so; 64 rows, 4096 keys, cap and bias: 227 and 145). A segment's
+// tiles are walked from its end: with a bias the newest keys hold the maximum, and the
+// reference of the softmax then hardly moves (each move is two barriers and a pass over
+// O^T). With a window the units are the tiles from the first one a query sees: the
+// others are never read.
 //
 // The weights. A slot's weight needs the row's final LSE, which no CTA has while
 // it walks. Each tile's shaped scores (fp32, R x 128) go to the workspace, 4 R
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // finish_kernel may take its places now; it waits for this grid's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_dependents();
   Walk w0;
   w0.b = start[0];
   w0.t = start[1];
@@ -1064,8 +1065,6 @@ __device__ __forceinline__ float pieces_lse(const DecodeTArgs& dt, const Pieces&
   return m + logf(tot);
 }
 
-__device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // What follows the ranges, in one launch. Blocks [0, merge_blocks): the merge of the
 // partials, one output row per warp: LSE = ln sum_c exp(LSE_c), O = sum_c exp(LSE_c -
 // LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
@@ -1083,7 +1082,7 @@ __global__ void __launch_bounds__(FIN_THREADS)
   const int R = dec.n_rows;
   if (static_cast<int>(blockIdx.x) < merge_blocks) {
     const long long rid = static_cast<long long>(blockIdx.x) * (FIN_THREADS / 32) + warp;
-    wait_primary();
+    wait_for_primary();
     if (rid >= static_cast<long long>(p.B) * p.H_kv * R) return;
     const int seg = static_cast<int>(rid / R);
     const int r = static_cast<int>(rid % R);
@@ -1144,8 +1143,8 @@ __global__ void __launch_bounds__(FIN_THREADS)
   int f, len;
   const int n = seq_tiles(seqs, b, f, len);
   const int t0 = f + (id % per) * FIN_TILES;
+  wait_for_primary();
   if (t0 >= n) return;
-  wait_primary();
   // The first rows' scores and the slots' weights are on their way while the LSEs form.
   const int t = t0 + warp;
   const bool on = t < n;

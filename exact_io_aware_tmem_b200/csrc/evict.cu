@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs 
   __shared__ int s_need, s_count, s_listed;
   const int hk = blockIdx.x % a.H_kv, b = blockIdx.x / a.H_kv, tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_dependents();
   const int len = a.cache_seqlens[b];
   if (len < 0 || len > a.max_len) {
     if (tid == 0) record_bounds(a.err, BAD_CACHE_LEN);
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const EvictArgs 
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictArgs a) {
   const int units = a.D / 8;
   const long long n = static_cast<long long>(a.B) * a.keep * a.H_kv * units;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection
+  wait_for_primary();   // the selection
   for (long long t = static_cast<long long>(blockIdx.x) * MOVE_THREADS + threadIdx.x; t < n;
        t += static_cast<long long>(gridDim.x) * MOVE_THREADS) {
     const int u = static_cast<int>(t % units);

@@ -37,6 +37,21 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams& p, const ShapeAr
   return {lo, hi};
 }
 
+// First entry of sequence b in the array of its 128-row query tiles' ranges: sequences
+// take ceil(len / 128) <= floor((start + len) / 128) - floor(start / 128) + 1 entries.
+__device__ __forceinline__ long long tile_base(const SeqInfo& s, int b) { return s.start / 128 + b; }
+
+// In a kernel launched before the one ahead of it in the stream has ended: until it has,
+// and its writes are seen. (Every CTA of such a kernel waits: its end stands for both.)
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the next kernel's CTAs take free places once every CTA of this grid has come here.
+__device__ __forceinline__ void release_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Decode over a cache: what fa_decode_shape adds to a decode's arguments.
 struct DecodeShapeArgs {
   float cap;
@@ -116,8 +131,10 @@ cudaError_t launch_shaped_fwd_f32(const AttnParams& p, const ShapeArgs& sh, cuda
 cudaError_t launch_shaped_bwd_f32(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_fwd.cu).
 cudaError_t launch_shaped_fwd(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
-// bf16: p.delta = D_i, and zeroes in p.dq_accum (shaped_delta.cu).
-cudaError_t launch_shaped_delta(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream);
+// bf16: p.delta = D_i, zeroes in p.dq_accum, and unless null the query tiles' key ranges
+// at tile_base (shaped_delta.cu).
+cudaError_t launch_shaped_delta(const AttnParams& p, const ShapeArgs& sh, int2* tiles,
+                                cudaStream_t stream);
 // bf16, D = 64 or 128 (shaped_bwd.cu): p.delta and p.dq_accum as for the fused
 // backward, ``tiles`` shaped_bwd_tiles_bytes() of scratch.
 size_t shaped_bwd_tiles_bytes(long long total, int B);
