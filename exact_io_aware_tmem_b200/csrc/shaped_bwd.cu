@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       atomicOr(p.err.word, ERR_BOUNDS);
       atomicExch(p.err.word + 1, BAD_ALIGN);
     }
+    wait_for_primary();
     return;
   }
 

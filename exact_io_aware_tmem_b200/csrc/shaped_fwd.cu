@@ -192,11 +192,12 @@ constexpr bool has_bias(int mode) { return mode == BIASED || mode == CAPPED_BIAS
 constexpr bool has_cap(int mode) { return mode >= CAPPED; }
 
 // z - m of 16 scores, their maximum into mx; with EXP P = 2^(z - m) as packed bf16 and
-// its sum. FORM: 0 and 1 the polynomials of the cap, 2 its exponential form.
+// its sum, with PARTIAL what packing added to it too. FORM: 0 and 1 the polynomials of
+// the cap, 2 its exponential form.
 template <int MODE, bool PARTIAL, bool EXP, int FORM>
 __device__ __forceinline__ void chunk(const uint32_t (&r)[16], int lo, int hi, int d0, float c2,
                                       const CapArgs& cap, float slope2, float m, float2 (&sum)[2],
-                                      float (&mx)[2], uint32_t* pk) {
+                                      float2& drift, float (&mx)[2], uint32_t* pk) {
   constexpr bool BIAS = has_bias(MODE);
   const float sl = d0 >= 0 ? -slope2 : slope2;
   const bool mixed = PARTIAL && BIAS && __any_sync(FULL, d0 < 0 && d0 + 15 > 0);
@@ -231,19 +232,25 @@ __device__ __forceinline__ void chunk(const uint32_t (&r)[16], int lo, int hi, i
       const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
       sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], make_float2(p0, p1));
       pk[i >> 1] = pack_bf16x2(p0, p1);
+      if (PARTIAL) {
+        const float2 held = make_float2(__uint_as_float(pk[i >> 1] << 16),
+                                        __uint_as_float(pk[i >> 1] & 0xffff0000u));
+        drift = __fadd2_rn(drift, __fadd2_rn(held, make_float2(-p0, -p1)));
+      }
     }
   }
 }
 
 // The thread's 64 scores of a tile, 16 at a time, the next 16 on their way. Returns the
-// largest z - m; with EXP P's sum is added to l, and P goes into pk or, in the fixed
-// mode, straight to TMEM.
+// largest z - m; with EXP P's sum is added to l, with PARTIAL too the rounding of its P to
+// drift, and P goes into pk or, in the fixed mode, straight to TMEM.
 template <int MODE, bool PARTIAL, bool EXP>
 __device__ __forceinline__ float half_tile(uint32_t s_col, const RowTile& t, float c2,
                                            const CapArgs& cap, float slope2, float m, float& l,
-                                           uint32_t* pk) {
+                                           float& drift, uint32_t* pk) {
   constexpr bool FIXED = MODE == CAPPED_FIXED;
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 dr = make_float2(0.f, 0.f);
   float mx[2] = {-INFINITY, -INFINITY};
   uint32_t r[2][16];
   tmem_ld16(s_col, r[0]);
@@ -258,7 +265,7 @@ __device__ __forceinline__ float half_tile(uint32_t s_col, const RowTile& t, flo
     if (c + 1 < HK / 16) tmem_ld16(s_col + 16 * (c + 1), r[(c + 1) & 1]);
     const int lo = t.lo - 16 * c, hi = t.hi - 16 * c, d0 = t.dist0 + 16 * c;
     if (!has_cap(MODE)) {
-      chunk<MODE, PARTIAL, EXP, 0>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
+      chunk<MODE, PARTIAL, EXP, 0>(q, lo, hi, d0, c2, cap, slope2, m, sum, dr, mx, to);
     } else {
       float ab[2] = {0.f, 0.f};
 #pragma unroll
@@ -267,16 +274,17 @@ __device__ __forceinline__ float half_tile(uint32_t s_col, const RowTile& t, flo
                                 fabsf(__uint_as_float(q[i + 1])));
       const int form = cap_form(cap, fmaxf(ab[0], ab[1]));
       if (form == 0)
-        chunk<MODE, PARTIAL, EXP, 0>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
+        chunk<MODE, PARTIAL, EXP, 0>(q, lo, hi, d0, c2, cap, slope2, m, sum, dr, mx, to);
       else if (form == 1)
-        chunk<MODE, PARTIAL, EXP, 1>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
+        chunk<MODE, PARTIAL, EXP, 1>(q, lo, hi, d0, c2, cap, slope2, m, sum, dr, mx, to);
       else
-        chunk<MODE, PARTIAL, EXP, 2>(q, lo, hi, d0, c2, cap, slope2, m, sum, mx, to);
+        chunk<MODE, PARTIAL, EXP, 2>(q, lo, hi, d0, c2, cap, slope2, m, sum, dr, mx, to);
     }
     // Columns 8 c .. 8 c + 7: scores that have been read.
     if (FIXED) tmem_st8(s_col + 8 * c, here);
   }
   if (EXP) l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+  if (EXP && PARTIAL) drift += dr.x + dr.y;
   return fmaxf(mx[0], mx[1]);
 }
 
@@ -541,6 +549,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     float m_ref = FIXED ? ceilf(cap.amp) - FIXED_TOP : -INFINITY;
     float last = -INFINITY;   // this half's maximum of the step before
     float l = 0.f;            // this half's part of the row's sum
+    // What the rounding of P to bf16 added to that, in tiles with masks: O is divided by
+    // l + drift, the sum of the P that it was made of, so that a row with one key is that
+    // key's V, and one with a few loses less. (Over whole tiles the roundings average out.)
+    float drift = 0.f;
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
       const int key0 = key_tile(bg + i) * BN + hf * HK;
@@ -560,6 +572,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       // means P_g V of the last one has), moves with the reference.
       auto rescale = [&](float alpha) {
         l *= alpha;
+        drift *= alpha;
         if (i == 0 || !__any_sync(FULL, alpha != 1.f)) return;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
@@ -589,20 +602,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           tmem_st16(s_col, z);
           tmem_st16(s_col + 16, z);
         } else if (whole) {
-          half_tile<MODE, false, true>(s_col, t, c2, cap, slope2, m_ref, l, nullptr);
+          half_tile<MODE, false, true>(s_col, t, c2, cap, slope2, m_ref, l, drift, nullptr);
         } else {
-          half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_ref, l, nullptr);
+          half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_ref, l, drift, nullptr);
         }
       } else {
         uint32_t pk[32];
-        float sum = 0.f, mx = -INFINITY;
+        float sum = 0.f, dr = 0.f, mx = -INFINITY;
         float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         if (none || !ok) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) pk[k] = 0u;
         } else {
-          mx = whole ? half_tile<MODE, false, true>(s_col, t, c2, cap, slope2, m_use, sum, pk)
-                     : half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, pk);
+          mx = whole ? half_tile<MODE, false, true>(s_col, t, c2, cap, slope2, m_use, sum, dr, pk)
+                     : half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, dr, pk);
         }
         bool again = rows_or(bar_id, mx > HIGH_LOG2 || !ok);
         if (!again && __any_sync(FULL, m_ref == -INFINITY)) {
@@ -616,9 +629,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         if (again) {
           if (!(ok = rows_and(bar_id, ok))) break;
           // The maximum first, of both halves, then P.
-          sum = 0.f;
+          sum = dr = 0.f;
           mx = -INFINITY;
-          if (!none) mx = half_tile<MODE, true, false>(s_col, t, c2, cap, slope2, 0.f, sum, pk);
+          if (!none) mx = half_tile<MODE, true, false>(s_col, t, c2, cap, slope2, 0.f, sum, dr, pk);
           s_row[hf * G * BM] = mx;
           if (!(ok = rows_and(bar_id, ok))) break;
           const float m_cand = fmaxf(mx, s_row[(hf ^ 1) * G * BM]);
@@ -630,11 +643,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           }
           rescale(alpha);
           m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          if (!none) mx = half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, pk);
+          if (!none) mx = half_tile<MODE, true, true>(s_col, t, c2, cap, slope2, m_use, sum, dr, pk);
         }
         last = m_use + mx;
         s_row[hf * G * BM] = last;
         l += sum;
+        drift += dr;
         uint32_t lo16[16], hi16[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -656,9 +670,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     s_row[hf * G * BM] = l;   // o_full: the partner has read the last maximum
     ok = rows_and(bar_id, ok);
     l += s_row[(hf ^ 1) * G * BM];
+    ok = rows_and(bar_id, ok);   // both have read
+    s_row[hf * G * BM] = drift;
+    ok = rows_and(bar_id, ok);
+    drift += s_row[(hf ^ 1) * G * BM];
     if (ok) {
       tc_fence_after();
-      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      const float inv_l = (l > 0.f) ? 1.f / (l + drift) : 0.f;
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];

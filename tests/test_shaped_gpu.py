@@ -236,6 +236,21 @@ def test_rows_all_at_one_end_of_the_cap(D, sign):
     inside("O", f64(o)[0], r.o, (HALF + 2 * e) * r.o_abs + HALF * np.abs(r.o))
 
 
+@pytest.mark.parametrize("cap,alibi", [(30.0, False), (0.0, True), (5.0, True), (0.0, False)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_with_one_key_is_its_value(D, cap, alibi):
+    # Whatever P is rounded to, O = P v / P: v to the rounding of the division (2^-23), so
+    # the same bf16.
+    n, H = 300, 2
+    q, k, v = (torch.randn(1, n, H, D, device="cuda").bfloat16() * 2 for _ in range(3))
+    slopes = torch.tensor([0.3, 0.1], device="cuda") if alibi else None
+    g = torch.Generator().manual_seed(4)
+    at = torch.randint(0, n, (1, n), generator=g, dtype=torch.int32).cuda()
+    o, _ = fa.fwd(q, k, v, softcap=cap or None, alibi_slopes=slopes, key_begin=at, key_end=at + 1)
+    clean()
+    assert torch.equal(o[0], v[0, at[0].long()])
+
+
 def test_ranges_that_see_nothing():
     q = torch.randn(2, 200, 4, 64, device="cuda", dtype=torch.bfloat16)
     z = torch.zeros(2, 200, dtype=torch.int32, device="cuda")
