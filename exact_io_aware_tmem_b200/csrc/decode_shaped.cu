@@ -11,10 +11,10 @@
 // What the shape adds. A thread owns one key and NH of the rows, so the cap (tanh by
 // a polynomial, or exponential and reciprocal), the bias (slope x distance of two positions) and the
 // window are a few instructions on a few scores. What a tile costs is then the latency
-// of the chain from its scores to its P: at NQ = 16 two threads share a key, beyond four
-// do, in groups of 128 threads that own their rows and never wait for one another (16
-// sequences, 32 rows a kv head, 4096 keys each: 98 us with two threads a key and one
-// barrier for all, 89 so; 64 rows, 4096 keys, cap and bias: 227 and 145). A segment's
+// of the chain from its scores to its P: four threads share a key, in groups of 128
+// threads that own their rows and never wait for one another (16 sequences, 32 rows a kv
+// head, 4096 keys each: 98 us with two threads a key and one barrier for all, 89 so; 64
+// rows, 4096 keys, cap and bias: 227 and 145; D = 64, 16 rows: 62 and 58). A segment's
 // tiles are walked from its end: with a bias the newest keys hold the maximum, and the
 // reference of the softmax then hardly moves (each move is two barriers and a pass over
 // O^T). With a window the units are the tiles from the first one a query sees: the
@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr uint32_t TILE = BN * D * 2;      // K / V tile
   static_assert(NQ == 16 || NQ == 32 || NQ == 64, "query columns");
   // Threads a key, each with NH of the query columns.
-  static constexpr int SPLIT = NQ == 16 ? 2 : 4;
+  static constexpr int SPLIT = 4;
   static constexpr int NH = NQ / SPLIT;
   static constexpr int SOFTMAX_THREADS = SPLIT * BN;
   static constexpr int THREADS = SOFTMAX_THREADS + 64;
@@ -231,11 +231,25 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// N (8, 16, 32) consecutive columns of this thread's TMEM lane, valid on
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// N (4, 8, 16) consecutive columns of this thread's TMEM lane, valid on
 // return.
 template <int N>
 __device__ __forceinline__ void tmem_row_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 8) {
+  if constexpr (N == 4) {
+    tmem_ld4(taddr, r);
+  } else if constexpr (N == 8) {
     tmem_ld8(taddr, r);
   } else {
 #pragma unroll
@@ -248,7 +262,9 @@ __device__ __forceinline__ void tmem_row_ld(uint32_t taddr, uint32_t (&r)[N]) {
 
 template <int N>
 __device__ __forceinline__ void tmem_row_st(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N == 8) {
+  if constexpr (N == 4) {
+    tmem_st4(taddr, r);
+  } else if constexpr (N == 8) {
     tmem_st8(taddr, r);
   } else {
 #pragma unroll
