@@ -49,13 +49,22 @@ struct Shared {
   int range[2];
 };
 
+// dkdv_kernel: PARTS steps at a time.
+template <int PARTS>
+struct SharedSteps {
+  float a[2][PARTS][TK][LD], b[2][PARTS][TK][LD];   // [buffer][part]
+  float own_a[WARPS][DMAX], own_b[WARPS][DMAX];
+  unsigned seen;   // which of 32 query tiles see a key of the CTA
+};
+
 // n rows (row stride ``stride``) of D floats into shared rows, 16 bytes at a time without
 // waiting where D allows; the rest of 32 rows and of D4 = D rounded up to four are zeros.
+template <int NT = THREADS>
 __device__ __forceinline__ void load_rows(float (*dst)[LD], const float* src, size_t stride, int n,
                                           int D, int D4) {
   if ((D & 3) == 0) {
     const int units = D4 / 4;
-    for (int t = threadIdx.x; t < TK * units; t += THREADS) {
+    for (int t = threadIdx.x; t < TK * units; t += NT) {
       const int r = t / units, u = t % units;
       const int bytes = r < n ? 16 : 0;   // 0: the 16 bytes become zeros
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(&dst[r][4 * u])),
@@ -63,7 +72,7 @@ __device__ __forceinline__ void load_rows(float (*dst)[LD], const float* src, si
                    : "memory");
     }
   } else {
-    for (int t = threadIdx.x; t < TK * D4; t += THREADS) {
+    for (int t = threadIdx.x; t < TK * D4; t += NT) {
       const int r = t / D4, d = t % D4;
       dst[r][d] = (r < n && d < D) ? src[r * stride + d] : 0.f;
     }
@@ -289,13 +298,19 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(AttnParams p, ShapeArgs sh)
   if (row) store_row(static_cast<float*>(p.dq) + off, acc, ln, D, p.scale);
 }
 
-// Every query of the sequence is looked at: a range tells which keys a query sees, not
-// which queries see a key. Tiles of 32 queries that see none of the CTA's keys are not
-// loaded.
-__global__ void __launch_bounds__(THREADS) dkdv_kernel(AttnParams p, ShapeArgs sh) {
+// Every query of the sequence is looked at, 1024 at a time: a range tells which keys a
+// query sees, not which queries see a key. Tiles of 32 queries that see none of the CTA's
+// keys are not loaded. A key row's chain of (tile, head) steps is the longest of the three
+// kernels', so with at most two CTAs a SM two warps share a row (PARTS 2), each with every
+// other step, and add up at the end: backward of B1 H4/2 D64 N600 165 us against 187, N1100
+// 327 against 423. With more CTAs the smaller shared memory of one warp a row lets more of
+// them run (B4 H8/2 N512 D64: 826 against 951).
+template <int PARTS>
+__global__ void __launch_bounds__(PARTS* THREADS) dkdv_kernel(AttnParams p, ShapeArgs sh) {
   extern __shared__ __align__(16) uint8_t raw[];
-  Shared& sm = *reinterpret_cast<Shared*>(raw);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int NT = PARTS * THREADS;
+  SharedSteps<PARTS>& sm = *reinterpret_cast<SharedSteps<PARTS>*>(raw);
+  const int warp = threadIdx.x / 32 % WARPS, part = threadIdx.x / THREADS, lane = threadIdx.x % 32;
   const int b = blockIdx.z, hk = blockIdx.y;
   const SeqInfo s = seq_info(p, b);
   if (!seq_ok(p, s) || static_cast<int>(blockIdx.x) * WARPS >= s.len) return;
@@ -304,68 +319,137 @@ __global__ void __launch_bounds__(THREADS) dkdv_kernel(AttnParams p, ShapeArgs s
   const int D = p.D, D4 = (D + 3) & ~3, g = p.H / p.H_kv;
   const size_t q_stride = static_cast<size_t>(p.H) * D;
   const size_t koff = (static_cast<size_t>(s.start + (row ? j : 0)) * p.H_kv + hk) * D;
-  load_own(sm.own_a[warp], static_cast<const float*>(p.k) + koff, D, D4);
-  load_own(sm.own_b[warp], static_cast<const float*>(p.v) + koff, D, D4);
+  if (part == 0) load_own(sm.own_a[warp], static_cast<const float*>(p.k) + koff, D, D4);
+  if (part == PARTS - 1) load_own(sm.own_b[warp], static_cast<const float*>(p.v) + koff, D, D4);
   const Lanes ln = lanes_of(D4);
   float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
   // Steps: the tiles of 32 queries that see a key of the CTA, and of each the g heads;
-  // the next step's rows load while this one's are worked on.
+  // the next pair's rows load while this one's are worked on.
+  const int base = p.causal ? static_cast<int>(blockIdx.x) * WARPS : 0;
+  const bool ranged = sh.key_begin != nullptr || sh.key_end != nullptr;
+  constexpr int GROUP = 32 * TK;
+  unsigned bits = 0;
+  int in_bits = -1;   // the group of 32 tiles that bits tells of
   struct Step {
-    int c0, h;
-    bool see;
-  };
-  auto seen = [&](int c0) {
-    const int i = c0 + lane;
-    if (!row || i >= s.len) return false;
-    const KeyRange kr = key_range(p, sh, s, i);
-    return j >= kr.lo && j < kr.hi;
+    int t, h;     // tile (queries base + 32 t ..), head of the group
+    bool on, see;
   };
   auto next = [&](Step st) {
-    if (st.c0 >= 0 && ++st.h < g) return st;
+    if (!st.on || (st.t >= 0 && ++st.h < g)) return st;
     st.h = 0;
-    st.c0 = st.c0 < 0 ? (p.causal ? static_cast<int>(blockIdx.x) * WARPS : 0) : st.c0 + TK;
-    for (; st.c0 < s.len; st.c0 += TK) {
-      st.see = seen(st.c0);
-      if (__syncthreads_or(st.see)) break;
+    for (++st.t;;) {
+      if (!ranged) {   // every tile from the first on sees them
+        st.on = base + TK * st.t < s.len;
+        if (!st.on) return st;
+        break;
+      }
+      if (st.t / 32 != in_bits) {
+        in_bits = st.t / 32;
+        st.on = base + in_bits * GROUP < s.len;
+        if (!st.on) return st;
+        __syncthreads();
+        if (threadIdx.x == 0) sm.seen = 0;
+        __syncthreads();
+        for (int x = threadIdx.x; x < GROUP; x += NT) {
+          const int i = base + in_bits * GROUP + x;
+          bool hit = false;
+          if (i < s.len) {
+            const KeyRange kr = key_range(p, sh, s, i);
+            hit = kr.lo < kr.hi && kr.lo < (static_cast<int>(blockIdx.x) + 1) * WARPS &&
+                  kr.hi > static_cast<int>(blockIdx.x) * WARPS;
+          }
+          if (__any_sync(FULL, hit) && lane == 0) atomicOr(&sm.seen, 1u << (x / TK));
+        }
+        __syncthreads();
+        bits = sm.seen;
+      }
+      const unsigned rest = bits >> (st.t & 31);
+      if (rest != 0) {
+        st.t += __ffs(rest) - 1;
+        break;
+      }
+      st.t = (in_bits + 1) * 32;
+    }
+    const int i = base + TK * st.t + lane;
+    st.see = false;
+    if (row && i < s.len) {
+      const KeyRange kr = key_range(p, sh, s, i);
+      st.see = j >= kr.lo && j < kr.hi;
     }
     return st;
   };
-  auto fetch = [&](const Step& st, int buf) {
-    if (st.c0 < s.len) {
-      const size_t off = (static_cast<size_t>(s.start + st.c0) * p.H + hk * g + st.h) * D;
-      const int n = min(TK, s.len - st.c0);
-      load_rows(sm.a[buf], static_cast<const float*>(p.q) + off, q_stride, n, D, D4);
-      load_rows(sm.b[buf], static_cast<const float*>(p.dout) + off, q_stride, n, D, D4);
+  auto fetch = [&](const Step& st, int buf, int k) {
+    if (!st.on) return;
+    const int c0 = base + TK * st.t;
+    const size_t off = (static_cast<size_t>(s.start + c0) * p.H + hk * g + st.h) * D;
+    const int n = min(TK, s.len - c0);
+    load_rows<NT>(sm.a[buf][k], static_cast<const float*>(p.q) + off, q_stride, n, D, D4);
+    load_rows<NT>(sm.b[buf][k], static_cast<const float*>(p.dout) + off, q_stride, n, D, D4);
+  };
+  Step st[PARTS];
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    st[k] = next(k ? st[k - 1] : Step{-1, 0, true, false});
+    fetch(st[k], 0, k);
+  }
+  loads_commit();
+  for (int buf = 0; st[0].on; buf ^= 1) {
+    Step nx[PARTS];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      nx[k] = next(k ? nx[k - 1] : st[PARTS - 1]);
+      fetch(nx[k], buf ^ 1, k);
     }
     loads_commit();
-  };
-  Step st = next({-1, 0, false});
-  fetch(st, 0);
-  for (int buf = 0; st.c0 < s.len; buf ^= 1) {
-    const Step nx = next(st);
-    fetch(nx, buf ^ 1);
     loads_wait();
     __syncthreads();
-    if (__any_sync(FULL, st.see)) {
-      const int i = st.c0 + lane, h = hk * g + st.h;
+    const Step me = PARTS > 1 && part ? st[PARTS - 1] : st[0];
+    if (me.on && __any_sync(FULL, me.see)) {
+      float(*const qs)[LD] = sm.a[buf][part];
+      float(*const gs)[LD] = sm.b[buf][part];
+      const int i = base + TK * me.t + lane, h = hk * g + me.h;
       float pij = 0.f, dx = 0.f;
-      if (st.see) {
+      if (me.see) {
         float grad;
-        const float z = shape(p, sh, sh.slopes ? sh.slopes[h] : 0.f,
-                              dot(sm.own_a[warp], sm.a[buf][lane], D4), i - j, grad);
+        const float z = shape(p, sh, sh.slopes ? sh.slopes[h] : 0.f, dot(sm.own_a[warp], qs[lane], D4),
+                              i - j, grad);
         pij = expf(z - p.lse[lse_index(p, b, h, s.start, i)]);
-        dx = pij * grad * (dot(sm.own_b[warp], sm.b[buf][lane], D4) -
+        dx = pij * grad * (dot(sm.own_b[warp], gs[lane], D4) -
                            p.delta[static_cast<size_t>(h) * p.total + s.start + i]);
       }
-      add_rows(dv, ln, pij, sm.b[buf]);
-      add_rows(dk, ln, dx, sm.a[buf]);
+      add_rows(dv, ln, pij, gs);
+      add_rows(dk, ln, dx, qs);
     }
     __syncthreads();
-    st = nx;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) st[k] = nx[k];
+  }
+  if constexpr (PARTS == 2) {
+    float4* const other = reinterpret_cast<float4*>(&sm.a[0][0][0][0]) + warp * 64 + lane;
+    if (part == 1) {
+      other[0] = dk;
+      other[32] = dv;
+    }
+    __syncthreads();
+    if (part == 1) return;
+    auto plus = [](float4& x, const float4& y) {
+      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    };
+    plus(dk, other[0]);
+    plus(dv, other[32]);
   }
   if (!row) return;
   store_row(static_cast<float*>(p.dk) + koff, dk, ln, D, p.scale);
   store_row(static_cast<float*>(p.dv) + koff, dv, ln, D, 1.f);
+}
+
+template <int PARTS>
+cudaError_t launch_dkdv(const AttnParams& p, const ShapeArgs& sh, int rows, cudaStream_t stream) {
+  using S = SharedSteps<PARTS>;
+  const cudaError_t e = allow_smem<dkdv_kernel<PARTS>>(sizeof(S));
+  if (e != cudaSuccess) return e;
+  dkdv_kernel<PARTS><<<dim3(rows, p.H_kv, p.B), PARTS * THREADS, sizeof(S), stream>>>(p, sh);
+  return cudaGetLastError();
 }
 
 }  // namespace f32
@@ -382,12 +466,12 @@ cudaError_t launch_shaped_fwd_f32(const AttnParams& p, const ShapeArgs& sh, cuda
 cudaError_t launch_shaped_bwd_f32(const AttnParams& p, const ShapeArgs& sh, cudaStream_t stream) {
   const int rows = (p.max_seqlen + f32::WARPS - 1) / f32::WARPS;
   cudaError_t e = allow_smem<f32::dq_kernel>(sizeof(f32::Shared));
-  if (e == cudaSuccess) e = allow_smem<f32::dkdv_kernel>(sizeof(f32::Shared));
   if (e != cudaSuccess) return e;
   f32::dq_kernel<<<dim3(rows, p.H, p.B), f32::THREADS, sizeof(f32::Shared), stream>>>(p, sh);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  f32::dkdv_kernel<<<dim3(rows, p.H_kv, p.B), f32::THREADS, sizeof(f32::Shared), stream>>>(p, sh);
-  return cudaGetLastError();
+  // Two CTAs a SM: see dkdv_kernel.
+  const bool few = static_cast<long long>(rows) * p.H_kv * p.B <= 2 * 148;
+  return few ? f32::launch_dkdv<2>(p, sh, rows, stream) : f32::launch_dkdv<1>(p, sh, rows, stream);
 }
 
 }  // namespace fa

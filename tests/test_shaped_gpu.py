@@ -167,6 +167,14 @@ def test_f32(D, H, H_kv, n, mask):
     run_case(D, "f32", [n, n], H, H_kv, D, False, mask == "any", 7.0, True, mask)
 
 
+@pytest.mark.parametrize("mask,causal", [("docs", True), ("window", False), ("prefix", False), ("none", True)])
+def test_f32_more_queries_than_one_look(mask, causal):
+    # The backward looks at 1024 queries' ranges at a time, and takes another form when
+    # there are many key rows.
+    for H, H_kv in ((2, 1), (6, 3)):
+        run_case(5 + H, "f32", [1100], H, H_kv, 16, False, causal, 7.0, True, mask)
+
+
 def test_f32_packed():
     run_case(3, "f32", [5, 0, 90, 1, 33], 4, 2, 32, True, True, 0.0, True, "any")
 
