@@ -500,7 +500,7 @@ fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, 
  *     visible: slot j <= slot i (causal) and pos_i - pos_j < window
  *   softcap, alibi_slopes  as above
  *   window         0: none
- *   key_positions  device int32 [B, H_kv, slots], >= 0 and ascending over a
+ *   key_positions  device int32 [B, H_kv, slots], >= 0, strictly ascending over a
  *                  sequence's slots, or NULL. (A query token before slot 0 has
  *                  its negative slot number for a position.)
  *   key_weights    device float32 [B, H_kv, slots] or NULL. Entry (b, hk, j),
