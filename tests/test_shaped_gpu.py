@@ -6,6 +6,10 @@ rounded to bf16 is off by at most 2^-8 of itself. With e the largest error of a
 score z in fp32 (the D products' sums, the cap, the base-2 exponent's rounding) plus
 1e-4 for the exponentials' own error (7.5e-5 at most):
   O    P rounded to bf16, O rounded:          (2^-8 + 2e) P|V| + 2^-8 |O|
+       In the forward's masked tiles the P that are summed are the rounded ones: with P_j
+       (1 + d_j), |d_j| <= 2^-8, O = sum (P + P d) V / sum (P + P d) is off by sum P d (V -
+       O) / (1 + sum P d) with P summing to 1, at most 2^-8 / (1 - 2^-8) (P|V| + |O|)
+       < 2^-8 (1 + 2^-7) (P|V| + |O|).
   LSE                                         e
   dV   as O:                                  (2^-8 + 2e) P^T|dO| + 2^-8 |dV|
   dQ   P (once more for dS) and dS rounded, D_i = sum P dP in fp32, dQ rounded:
@@ -117,7 +121,8 @@ def run_case(seed, dtype, lengths, H, H_kv, D, varlen, causal, cap, alibi, mask,
     h = HALF if dtype == "bf16" else 2.0 ** -23
     lse_ht = f64(lse) if varlen else f64(lse).transpose(1, 0, 2).reshape(H, T)
     inside("LSE", lse_ht, r.lse, e)
-    inside("O", f64(o).reshape(T, H, D), r.o, (h + 2 * e) * r.o_abs + h * np.abs(r.o))
+    inside("O", f64(o).reshape(T, H, D), r.o,
+           (h * (1 + 2 * h) + 2 * e) * (r.o_abs + np.abs(r.o)) + h * np.abs(r.o))
     if backward:
         got = fa.bwd(do, q, k, v, o, lse, **kw)
         clean()
