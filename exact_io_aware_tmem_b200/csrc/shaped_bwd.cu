@@ -28,7 +28,7 @@
 // - The cap per 32 scores by the shortest polynomial that their largest allows, or by
 //   exponential and reciprocal (score_cap.cuh).
 //
-// B1 H16/4 N8192 D128 causal, cap 50: 980 us of a 1570 us step, 700 TFLOP/s (the unshaped
+// B1 H16/4 N8192 D128 causal, cap 50: 980 us of a 1530 us step, 700 TFLOP/s (the unshaped
 // fused backward takes 859 with its D); bound by the chain of the warps that form P and
 // dX, which the cap and 1 - t^2 lengthen, as the unshaped one is by its own.
 #include <cuda_fp16.h>
