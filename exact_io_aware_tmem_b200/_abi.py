@@ -79,6 +79,9 @@ SIGNATURES = {
     "fa_decode_shaped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_ll,
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "fa_selftest_decode_finish": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                          c_int, c_int, c_void_p, c_ll, c_void_p, c_size_t,
+                                          c_void_p]),
     "fa_cache_evict_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "fa_cache_evict": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                c_int, c_ll, c_int, c_void_p, c_void_p, c_ll, c_int, c_int,

@@ -1059,10 +1059,13 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
   }
 }
 
-// Range of group partials [c0, c1] of a segment; false when its CTA wrote the rows
-// (one piece) or the sequence is empty.
+// Range of group partials [c0, c1] of a segment with keys; c0 == c1 when its CTA wrote the
+// rows (one piece).
 struct Pieces {
   int c0, c1;
+  // Whether the partials lie in the workspace. They do not where a wait of the first kernel
+  // ran out: a CTA that gives up leaves the entries as it found them.
+  __device__ bool sound(int groups) const { return c0 >= 0 && c1 < groups && c0 <= c1; }
 };
 __device__ __forceinline__ Pieces seg_pieces(const DecodeTArgs& dt, int seg, int len) {
   if (len <= 0) return {0, -1};
@@ -1107,11 +1110,11 @@ __global__ void __launch_bounds__(FIN_THREADS)
     const int len = __ldg(dec.cache_seqlens + b);
     if (len < 0 || len > p.max_seqlen) return;   // reported by the partials kernel
     const Pieces pc = seg_pieces(dt, seg, len);
-    if (len > 0 && pc.c0 == pc.c1) return;   // one piece: its CTA wrote the row
-    if (len > 0 && (pc.c0 < 0 || pc.c1 >= dt.ctas / p.H_kv || pc.c0 > pc.c1)) {
+    if (len > 0 && !pc.sound(dt.ctas / p.H_kv)) {
       if (lane == 0) record_bounds(p.err, BAD_MERGE);
       return;
     }
+    if (len > 0 && pc.c0 == pc.c1) return;   // one piece: its CTA wrote the row
     const size_t orow = static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H + hk * dec.g +
                         r % dec.g;
     constexpr int PER = D / 32;   // columns per lane
@@ -1175,9 +1178,13 @@ __global__ void __launch_bounds__(FIN_THREADS)
   float old[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) old[k] = (on && t * BN + 4 * lane + k < len) ? dst[k] : 0.f;
+  const Pieces pc = seg_pieces(dt, seg, len);   // (len > 0: the segment has tiles)
+  if (!pc.sound(dt.ctas / p.H_kv)) {   // the block's one segment: nothing is added to it
+    if (threadIdx.x == 0) record_bounds(p.err, BAD_MERGE);
+    return;
+  }
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
-    const Pieces pc = seg_pieces(dt, seg, len);
     const float s = pc.c0 == pc.c1 ? p.lse[static_cast<size_t>(b * dec.q_len + r / dec.g) * p.H +
                                            hk * dec.g + r % dec.g]
                                    : pieces_lse(dt, pc, b, hk, p.H_kv, R, r);
@@ -1246,9 +1253,15 @@ cudaError_t launch_nq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   return cudaGetLastError();
 }
 
+Lens lens_of(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh) {
+  const long long reach = sh.window > 0 ? static_cast<long long>(sh.window) + d.q_len - 1 : INT_MAX;
+  return {d.cache_seqlens, p.B, p.max_seqlen,
+          static_cast<int>(min(reach, static_cast<long long>(INT_MAX)))};
+}
+
 template <int D>
-cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh,
-                     const Workspace& w, cudaStream_t stream) {
+cudaError_t launch_walk(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh,
+                        const Workspace& w, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   const unsigned box_rows =
       (d.block_table != nullptr) ? static_cast<unsigned>(min(d.page, BN)) : BN;
@@ -1258,17 +1271,16 @@ cudaError_t launch_d(const AttnParams& p, const DecodeArgs& d, const DecodeShape
       !make_tmap_bf16_2d(&tk, p.k, d.cache_rows, cols, 64, box_rows) ||
       !make_tmap_bf16_2d(&tv, p.v, d.cache_rows, cols, 64, box_rows))
     return cudaErrorInvalidValue;
-  const long long reach = sh.window > 0 ? static_cast<long long>(sh.window) + d.q_len - 1 : INT_MAX;
-  const Lens seqs = {d.cache_seqlens, p.B, p.max_seqlen,
-                     static_cast<int>(min(reach, static_cast<long long>(INT_MAX)))};
-  cudaError_t e;
-  if (d.n_rows <= 16)
-    e = launch_nq<D, 16>(tq, tk, tv, p, d, sh, w, seqs, stream);
-  else if (d.n_rows <= 32)
-    e = launch_nq<D, 32>(tq, tk, tv, p, d, sh, w, seqs, stream);
-  else
-    e = launch_nq<D, 64>(tq, tk, tv, p, d, sh, w, seqs, stream);
-  if (e != cudaSuccess) return e;
+  const Lens seqs = lens_of(p, d, sh);
+  if (d.n_rows <= 16) return launch_nq<D, 16>(tq, tk, tv, p, d, sh, w, seqs, stream);
+  if (d.n_rows <= 32) return launch_nq<D, 32>(tq, tk, tv, p, d, sh, w, seqs, stream);
+  return launch_nq<D, 64>(tq, tk, tv, p, d, sh, w, seqs, stream);
+}
+
+template <int D>
+cudaError_t launch_finish(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh,
+                          const Workspace& w, cudaStream_t stream) {
+  const Lens seqs = lens_of(p, d, sh);
   const long long rows = static_cast<long long>(p.B) * p.H_kv * d.n_rows;
   const int tiles_max = (p.max_seqlen + BN - 1) / BN;
   const int walked = static_cast<int>(
@@ -1305,8 +1317,17 @@ cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,
                                  const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream) {
   const sdec::Workspace w = sdec::carve(workspace, p.B, p.H_kv, d.n_rows, p.D, p.max_seqlen,
                                         sh.key_weights != nullptr);
-  return p.D == 64 ? sdec::launch_d<64>(p, d, sh, w, stream)
-                   : sdec::launch_d<128>(p, d, sh, w, stream);
+  const cudaError_t e = p.D == 64 ? sdec::launch_walk<64>(p, d, sh, w, stream)
+                                  : sdec::launch_walk<128>(p, d, sh, w, stream);
+  return e == cudaSuccess ? launch_decode_finish(p, d, sh, workspace, stream) : e;
+}
+
+cudaError_t launch_decode_finish(const AttnParams& p, const DecodeArgs& d,
+                                 const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream) {
+  const sdec::Workspace w = sdec::carve(workspace, p.B, p.H_kv, d.n_rows, p.D, p.max_seqlen,
+                                        sh.key_weights != nullptr);
+  return p.D == 64 ? sdec::launch_finish<64>(p, d, sh, w, stream)
+                   : sdec::launch_finish<128>(p, d, sh, w, stream);
 }
 
 }  // namespace fa

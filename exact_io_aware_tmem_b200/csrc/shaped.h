@@ -147,6 +147,9 @@ size_t decode_shaped_workspace(long long B, int H_kv, long long n_rows, int D, i
                                bool weights);
 cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,
                                  const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream);
+// Its second kernel alone: the merge, and the weights.
+cudaError_t launch_decode_finish(const AttnParams& p, const DecodeArgs& d,
+                                 const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace fa

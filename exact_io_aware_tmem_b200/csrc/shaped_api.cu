@@ -188,6 +188,32 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
       fa::launch_decode_shaped(p, d, a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+fa_status fa_selftest_decode_finish(void* o, float* lse, const int* cache_seqlens, int B,
+                                    int q_len, int H, int H_kv, int D, int max_seqlen_k,
+                                    float* key_weights, long long slots, void* workspace,
+                                    size_t ws_bytes, fa_stream_t stream) {
+  AttnParams p = {};
+  fa::DecodeArgs d = {};
+  bool empty = false;
+  const fa_status st = fa::check_decode(p, d, empty, o, o, o, o, lse, cache_seqlens, nullptr, B,
+                                        q_len, H, H_kv, D, max_seqlen_k, 0,
+                                        static_cast<long long>(B) * max_seqlen_k, max_seqlen_k, 1,
+                                        0.f);
+  if (st != FA_OK || empty) return st;
+  if (d.n_rows > 64) return FA_ERR_UNSUPPORTED;
+  if (!key_weights || slots < max_seqlen_k) return FA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !fa::aligned16(workspace) ||
+      ws_bytes < fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k, 1))
+    return FA_ERR_INVALID_ARG;
+  p.err.word = fa::err_word();
+  if (p.err.word == nullptr) return FA_ERR_CUDA;
+  fa::DecodeShapeArgs a = {};
+  a.key_weights = key_weights;
+  a.slots = slots;
+  return fa::record_cuda(
+      fa::launch_decode_finish(p, d, a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t fa_cache_evict_workspace_size(int B, int H_kv, int keep) {
   if (B <= 0 || H_kv <= 0 || keep <= 0) return 0;
   return fa::round256(static_cast<size_t>(B) * H_kv * keep * 4);

@@ -510,7 +510,8 @@ fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, 
  *   slots          row length of the two, >= max_seqlen_k
  * The rest as for fa_decode with n_split = 0, but at most 64 query rows share
  * a key/value head (q_len * H / H_kv <= 64, else FA_ERR_UNSUPPORTED). Results
- * are bitwise reproducible.
+ * are bitwise reproducible. After FA_ERR_DEVICE_TIMEOUT key_weights, as the outputs,
+ * may hold anything.
  */
 typedef struct {
   float softcap;
@@ -532,6 +533,19 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
                            long long cache_rows, int max_seqlen_k, int causal, float scale,
                            const fa_decode_shape* shape, void* workspace, size_t ws_bytes,
                            fa_stream_t stream);
+
+/*
+ * fa_selftest_decode_finish - enqueues only the second kernel of fa_decode_shaped
+ * (the merge and the weights) on ``workspace`` as it is, which stands for what the
+ * first kernel leaves when one of its waits ran out. For the library's own tests: a
+ * (sequence, kv head) whose entries point outside the workspace is reported by
+ * fa_check_device_error as FA_ERR_INVALID_ARG, and its rows of o, lse and key_weights
+ * are left as they are. Arguments as for fa_decode_shaped with key_weights.
+ */
+fa_status fa_selftest_decode_finish(void* o, float* lse, const int* cache_seqlens, int B,
+                                    int q_len, int H, int H_kv, int D, int max_seqlen_k,
+                                    float* key_weights, long long slots, void* workspace,
+                                    size_t ws_bytes, fa_stream_t stream);
 
 /*
  * fa_cache_evict - copies the slots worth keeping of a bf16 cache into another

@@ -1,0 +1,86 @@
+"""Edges of the shaped entry points on the GPU: workspaces in a bad state, values far from
+the usual, rows that belong to nobody, recipes of the documentation."""
+import pytest
+import torch
+
+import exact_io_aware_tmem_b200 as fa
+from exact_io_aware_tmem_b200 import _abi
+from tests.test_shaped_gpu import clean
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from exact_io_aware_tmem_b200 import build
+    build.build()
+
+
+# ------------------------------- what a timed-out first kernel leaves behind ---
+
+class _Decode:
+    """One decode's arguments; its workspace, and where the segments' first and last
+    group lie in it."""
+
+    def __init__(self, D=128, H=8, H_kv=2, lengths=(700, 40)):
+        g = torch.Generator("cuda").manual_seed(D)
+        rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+        self.B, self.H, self.H_kv, self.D, self.most = len(lengths), H, H_kv, D, max(lengths)
+        self.q = rnd(self.B, H, D)
+        self.k, self.v = (rnd(self.B * self.most, H_kv, D) for _ in range(2))
+        self.lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        self.lib = _abi.lib()
+        self.need = self.lib.fa_decode_shaped_workspace_size(self.B, 1, H, H_kv, D, self.most, 1)
+        self.ws = torch.empty(self.need, dtype=torch.uint8, device="cuda")
+        self.w = torch.rand(self.B, H_kv, self.most, generator=g, device="cuda")
+        self.groups = torch.cuda.get_device_properties(0).multi_processor_count // H_kv
+        up = lambda n: -(-n // 256) * 256
+        rows, segs = (self.B + self.groups) * H_kv * (H // H_kv), self.B * H_kv
+        at = up(rows * D * 4) + up(rows * 4)
+        ints = lambda o: self.ws[o:o + 4 * segs].view(torch.int32)
+        self.first, self.last = ints(at), ints(at + up(segs * 4))
+
+    def run(self):
+        return fa.decode(self.q, self.k, self.v, self.lens, q_len=1, max_seqlen_k=self.most,
+                         softcap=30.0, key_weights=self.w, workspace=self.ws)
+
+    def finish(self, o, lse):
+        _abi.check(self.lib.fa_selftest_decode_finish(
+            o.data_ptr(), lse.data_ptr(), self.lens.data_ptr(), self.B, 1, self.H, self.H_kv, self.D,
+            self.most, self.w.data_ptr(), self.most, self.ws.data_ptr(), self.need,
+            torch.cuda.current_stream().cuda_stream), "fa_selftest_decode_finish")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_finish_on_a_sound_workspace_adds_the_weights_again(D):
+    d = _Decode(D)
+    d.w.zero_()
+    o, lse = d.run()
+    clean()
+    once, o1, lse1 = d.w.clone(), o.clone(), lse.clone()
+    assert (d.first >= 0).all() and (d.first <= d.last).all() and (d.last < d.groups).all()
+    d.finish(o, lse)
+    clean()
+    assert torch.equal(d.w, once + once)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("first,last", [(-1, -1), (0, "groups"), (3, 1), (-5, 2), (MOST, MOST),
+                                        (-MOST - 1, MOST), ("groups", "groups")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_finish_reports_pieces_outside_the_workspace(D, first, last):
+    d = _Decode(D)
+    d.ws.fill_(0xFF)   # NaN, -1
+    d.first.fill_(d.groups if first == "groups" else first)
+    d.last.fill_(d.groups if last == "groups" else last)
+    o = torch.full((d.B, d.H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((d.B, d.H), 5.0, device="cuda")
+    w0 = d.w.clone()
+    d.finish(o, lse)
+    st, where = fa.check_device_error()
+    assert st == _abi.FA_ERR_INVALID_ARG and where == 0xE0F03
+    assert torch.equal(d.w, w0) and (o == 3.0).all() and (lse == 5.0).all()
+    clean()

@@ -1,0 +1,24 @@
+"""Edges of the shaped entry points without a GPU."""
+import pytest
+
+from exact_io_aware_tmem_b200 import _abi
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from exact_io_aware_tmem_b200 import build
+    build.build()
+    return _abi.lib()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), _abi.FA_OK), (dict(o=None), _abi.FA_ERR_INVALID_ARG),
+    (dict(weights=None), _abi.FA_ERR_INVALID_ARG), (dict(slots=99), _abi.FA_ERR_INVALID_ARG),
+    (dict(ws=None), _abi.FA_ERR_INVALID_ARG), (dict(ws=264), _abi.FA_ERR_INVALID_ARG),
+    (dict(ws_bytes=1), _abi.FA_ERR_INVALID_ARG), (dict(H=130), _abi.FA_ERR_UNSUPPORTED),
+    (dict(D=96), _abi.FA_ERR_UNSUPPORTED), (dict(max_len=0), _abi.FA_ERR_INVALID_ARG)])
+def test_selftest_decode_finish_arguments(lib, kw, code):
+    a = dict(o=256, lse=256, lens=256, B=2, q_len=1, H=4, H_kv=2, D=64, max_len=100, weights=256,
+             slots=100, ws=256, ws_bytes=1 << 30)
+    a.update(kw)
+    assert lib.fa_selftest_decode_finish(*a.values(), None) == code
