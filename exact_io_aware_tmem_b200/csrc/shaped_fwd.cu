@@ -177,13 +177,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// Under a cap and without a bias the scores lie in [-A, A], and while A <= 90 no
-// maximum is needed: with the reference m = ceil(A) - 80, P = 2^(x - m) lies in
-// [2^-101, 2^80] whatever the row holds; bf16 and fp32 keep their relative precision
-// over that range, and the sums stay below 2^127 for 2^31 keys of |v| up to 2^16. No
-// half waits for the other and O is never rescaled.
-constexpr float FIXED_AMP = 90.f;
-constexpr float FIXED_TOP = 80.f;
+// Under a cap and without a bias the scores lie in [-A, A], and while A <= 74 (a cap of
+// 51) no maximum is needed: with the reference m = max(0, ceil(A) - 64), P = 2^(x - m) lies
+// in [2^-84, 2^64] whatever the row holds. No half waits for the other and O is never
+// rescaled: B2 H16 N8192 D128 causal 562 us under a cap just inside, 692 with the running
+// maximum. The top is the one that a running maximum allows too (HIGH_LOG2), so that O
+// overflows in no mode while the |v| of a query's keys add up to less than 2^63; at the
+// other end P v keeps fp32's precision for |v| from 2^-42 on.
+constexpr float FIXED_AMP = 74.f;
 
 // MODE: which parts of the shape the scores have (key ranges always).
 enum Mode : int { RANGES = 0, BIASED = 1, CAPPED = 2, CAPPED_BIASED = 3, CAPPED_FIXED = 4 };
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     const int bg = g ? b_1 : b_0, n = (g ? f_1 : f_0) - bg;
     const float c2 = p.scale_log2;
     const float slope2 = BIAS ? __ldg(sh.slopes + h) * LOG2E : 0.f;
-    float m_ref = FIXED ? ceilf(cap.amp) - FIXED_TOP : -INFINITY;
+    float m_ref = FIXED ? fmaxf(0.f, ceilf(cap.amp) - HIGH_LOG2) : -INFINITY;
     float last = -INFINITY;   // this half's maximum of the step before
     float l = 0.f;            // this half's part of the row's sum
     // What the rounding of P to bf16 added to that, in tiles with masks: O is divided by

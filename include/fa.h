@@ -433,7 +433,10 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v, const float*
  *                 (0 / the sequence's length). Entries outside the sequence
  *                 are clipped to it; begin >= end means no key.
  * Every element of q, k, v and dout must be finite, of tokens that no query
- * sees too: a masked probability is 0 and multiplies what lies there.
+ * sees too: a masked probability is 0 and multiplies what lies there. In bf16 the |v|
+ * of the keys that a query sees must add up to less than 2^63 (they are summed in fp32
+ * with factors of up to 2^64 before the division), and those below 2^-42 are exact to
+ * 2^-42 only.
  * A NULL shape, or one with nothing set, is fa_fwd / fa_bwd.
  */
 typedef struct {

@@ -1,11 +1,14 @@
 """Edges of the shaped entry points on the GPU: workspaces in a bad state, values far from
 the usual, rows that belong to nobody, recipes of the documentation."""
+import numpy as np
 import pytest
 import torch
 
 import exact_io_aware_tmem_b200 as fa
 from exact_io_aware_tmem_b200 import _abi
-from tests.test_shaped_gpu import clean
+from oracle import shaped as osh
+from tests._util import f64
+from tests.test_shaped_gpu import HALF, clean, inside, score_error
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +87,40 @@ def test_decode_finish_reports_pieces_outside_the_workspace(D, first, last):
     assert st == _abi.FA_ERR_INVALID_ARG and where == 0xE0F03
     assert torch.equal(d.w, w0) and (o == 3.0).all() and (lse == 5.0).all()
     clean()
+
+
+# ------------------------------------------------------- values far from one ---
+
+@pytest.mark.parametrize("log2_v", [50, -20])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("cap,alibi", [(1.0, False), (10.0, False), (44.0, False), (45.0, False),
+                                       (51.0, False), (52.0, False), (62.0, False), (200.0, False),
+                                       (20.0, True), (0.0, True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_and_small_values_at_either_end_of_the_cap(D, cap, alibi, sign, log2_v):
+    # Every score of a row at the same end of the cap. 300 keys of |v| below 2^53: less than
+    # 2^62 in all. The bounds are relative to |v|, as everywhere.
+    n, H = 300, 2
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn((n, H, D), generator=g).abs() * 8
+    k = sign * torch.randn((n, H, D), generator=g).abs() * 8
+    v = torch.randn((n, H, D), generator=g) * 2.0 ** log2_v
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    scale = 1.0 if cap else 2.0 ** -10
+    slopes = torch.tensor([0.3, 0.1]) if alibi else None
+    o, lse = fa.fwd(*(x.cuda()[None] for x in (q, k, v)), causal=True, softcap=cap or None, scale=scale,
+                    alibi_slopes=None if slopes is None else slopes.cuda())
+    clean()
+    r = osh.forward(q, k, v, [0, n], True, scale, cap, slopes)
+    e = score_error(q, k, scale, cap, slopes, n, "bf16")
+    if cap:
+        # The part of e that is the product's error, D 2^-24 scale |q||k|, reaches z by 1 - tanh^2
+        # <= 4 e^(-2 u).
+        dot = D * 2.0 ** -24 * scale * (abs(f64(q)).max(0) ** 2).sum(-1).max() ** 0.5 * \
+            (abs(f64(k)).max(0) ** 2).sum(-1).max() ** 0.5
+        low = min(abs(scale * f64(q)[:, h] @ f64(k)[:, h].T).min() for h in range(H))
+        z = cap + (0.0 if slopes is None else float(slopes.max()) * n)
+        e = dot * 4 * np.exp(-2 * low / cap) + 2.0 ** -21 * (2 + z + cap) + 1e-4
+    inside("LSE", f64(lse)[0], r.lse, e)
+    # As in the masked tiles of other cases: the P that are summed are the rounded ones.
+    inside("O", f64(o)[0], r.o, (HALF * (1 + 2 * HALF) + 2 * e) * (r.o_abs + abs(r.o)) + HALF * abs(r.o))
