@@ -851,6 +851,8 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
         float most = 0.f;
 #pragma unroll
         for (int r = 0; r < NH; ++r) most = fmaxf(most, fabsf(__uint_as_float(s[r])));
+        // What lies past the end, or before every query's window, must not choose the form.
+        if (key >= w.len || key < first_slot(seqs, w.len)) most = 0.f;
         if (cap_form(cap, most) == 0) {
 #pragma unroll
           for (int r = 0; r < NH; r += 2) {

@@ -513,7 +513,7 @@ fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, 
  *   slots          row length of the two, >= max_seqlen_k
  * The rest as for fa_decode with n_split = 0, but at most 64 query rows share
  * a key/value head (q_len * H / H_kv <= 64, else FA_ERR_UNSUPPORTED). Results
- * are bitwise reproducible. After FA_ERR_DEVICE_TIMEOUT key_weights, as the outputs,
+ * are bitwise reproducible, whatever lies past a sequence's end. After FA_ERR_DEVICE_TIMEOUT key_weights, as the outputs,
  * may hold anything.
  */
 typedef struct {

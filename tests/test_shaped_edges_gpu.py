@@ -124,3 +124,55 @@ def test_large_and_small_values_at_either_end_of_the_cap(D, cap, alibi, sign, lo
     inside("LSE", f64(lse)[0], r.lse, e)
     # As in the masked tiles of other cases: the P that are summed are the rounded ones.
     inside("O", f64(o)[0], r.o, (HALF * (1 + 2 * HALF) + 2 * e) * (r.o_abs + abs(r.o)) + HALF * abs(r.o))
+
+
+# ------------------------------------------------------ rows that are nobody's ---
+
+@pytest.mark.parametrize("page", [None, 64])
+@pytest.mark.parametrize("q_len,window,alibi", [(1, 0, False), (5, 0, True), (2, 100, False)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_bits_do_not_depend_on_rows_past_the_end(D, q_len, window, alibi, page):
+    # Stale tokens, or anything else, behind a sequence's length: the results are the same bits.
+    g = torch.Generator("cuda").manual_seed(D)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    lengths, most = [70, 300, 129], 448
+    q, k, v = rnd(3 * q_len, 8, D), rnd(3 * most, 2, D), rnd(3 * most, 2, D)
+    kw = dict(q_len=q_len, max_seqlen_k=most, softcap=30.0, window=window or None,
+              page_size=page or most)
+    if page:
+        kw["block_table"] = torch.arange(3 * most // page, dtype=torch.int32, device="cuda").view(3, -1)
+    if alibi:
+        kw["alibi_slopes"] = torch.linspace(0.01, 0.2, 8, device="cuda")
+    outs = []
+    for fill in (0.0, 1.0, 100.0, float("inf"), float("nan")):
+        for b, n in enumerate(lengths):
+            k[b * most + n:(b + 1) * most] = fill
+            v[b * most + n:(b + 1) * most] = fill
+        w = torch.zeros(3, 2, most, device="cuda")
+        outs.append((*fa.decode(q, k, v, torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                                key_weights=w, **kw), w))
+        clean()
+    for o in outs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_bits_do_not_depend_on_pages_before_the_window(D):
+    # The pages that no query sees hold large keys, or have been given back.
+    n, window, page = 700, 100, 16
+    g = torch.Generator("cuda").manual_seed(D)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    q, k, v = rnd(2, 8, D), rnd(704, 2, D), rnd(704, 2, D)
+    gone = (n - window - 1) // page   # pages of slots that neither of the two queries sees
+    k[:gone * page] = 100.0
+    table = torch.arange(704 // page, dtype=torch.int32, device="cuda")[None]
+    freed = table.clone()
+    freed[:, :gone] = -1
+    outs = []
+    for t in (table, freed):
+        w = torch.zeros(1, 2, n, device="cuda")
+        outs.append((*fa.decode(q, k, v, torch.tensor([n], dtype=torch.int32, device="cuda"), q_len=2,
+                                max_seqlen_k=n, block_table=t, page_size=page, window=window,
+                                softcap=30.0, key_weights=w), w))
+        clean()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
