@@ -406,12 +406,13 @@ def _decode_shaped(q, k_cache, v_cache, cache_seqlens, q_len, max_seqlen_k, bloc
         _aux(key_positions, "key_positions", torch.int32, side, dev),
         _aux(key_weights, "key_weights", torch.float32, side, dev), slots)
     lib = _lib()
+    span = max_seqlen_k if not window or window < 0 else min(max_seqlen_k, int(window) + q_len + 127)
     if dev.index == torch.cuda.current_device():
-        need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, max_seqlen_k,
+        need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, span,
                                    int(key_weights is not None))
     else:
         with torch.cuda.device(dev):
-            need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, max_seqlen_k,
+            need = _decode_shaped_need(lib, dev.index, B, q_len, H, H_kv, D, span,
                                        int(key_weights is not None))
     if need and (workspace is None or _room(workspace, dev) < need):
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)

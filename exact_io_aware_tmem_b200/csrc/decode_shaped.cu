@@ -21,7 +21,7 @@
 // others are never read.
 //
 // The weights. A slot's weight needs the row's final LSE, which no CTA has while
-// it walks. Each tile's shaped scores (fp32, R x 128) go to the workspace, 4 R
+// it walks. Each walked tile's shaped scores (fp32, R x 128) go to the workspace, 4 R
 // bytes a key beside the 4 D bytes of K and V (3 % at R = 4, D = 128; 25 % at R = 32),
 // and the second kernel forms sum_r 2^(z_r - LSE_r) per slot from them: no second pass
 // over K, no atomics, a fixed order. K and V are read once, so their tiles are loaded to
@@ -277,7 +277,8 @@ __device__ __forceinline__ void tmem_row_st(uint32_t taddr, const uint32_t (&r)[
 struct Lens {
   const int* lens;
   int B, max_len;
-  int reach;   // slots before the last token that some query may see (window), or max_len
+  int reach;   // slots before the last token that some query may see (window), or INT_MAX
+  int tiles;   // the most tiles of a sequence that are walked
 };
 
 // First slot some query of the sequence may see. Positions of a cache that lost
@@ -754,7 +755,6 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
     const int g = dec.g;
     const bool capped = sh.cap > 0.f, biased = sh.slopes != nullptr;
     const bool placed = sh.key_positions != nullptr;
-    const int tiles_max = (p.max_seqlen + BN - 1) / BN;
     // This thread's P word for a row pair holds keys (kt & ~1, kt | 1) of
     // row r (even thread) or r + 1 (odd thread): the pair's column block,
     // 16-byte unit (swizzled by the row below) and byte in the unit.
@@ -894,7 +894,8 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
             x[r] = -INFINITY;
       }
       if (xs != nullptr) {
-        float* dst = xs + ((static_cast<size_t>(w.b) * p.H_kv + hk) * tiles_max + w.t) * R * BN + kt;
+        float* dst =
+            xs + ((static_cast<size_t>(w.b) * p.H_kv + hk) * seqs.tiles + w.t - w.f) * R * BN + kt;
 #pragma unroll
         for (int r = 0; r < NH; ++r)
           if (r0 + r < R) dst[(r0 + r) * BN] = x[r];
@@ -1091,14 +1092,13 @@ __device__ __forceinline__ float pieces_lse(const DecodeTArgs& dt, const Pieces&
 // LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
 // get O = 0 and LSE = -inf here. The others: key_weights[b, hk, j] += sum_r 2^(z_rj -
 // LSE_r log2 e), FIN_TILES tiles of a segment per block, a warp a tile, four slots a lane.
-// `walked`: the most tiles a segment can have, from the first one that a query sees.
 constexpr int FIN_THREADS = 128;
 constexpr int FIN_TILES = FIN_THREADS / 32;
 template <int D>
 __global__ void __launch_bounds__(FIN_THREADS)
     finish_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt,
                   const DecodeShapeArgs sh, const Lens seqs, const float* __restrict__ xs,
-                  int merge_blocks, int tiles_max, int walked) {
+                  int merge_blocks) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int R = dec.n_rows;
   if (static_cast<int>(blockIdx.x) < merge_blocks) {
@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(FIN_THREADS)
     return;
   }
   __shared__ float lse2[64];
-  const int per = (walked + FIN_TILES - 1) / FIN_TILES;
+  const int per = (seqs.tiles + FIN_TILES - 1) / FIN_TILES;
   const int id = static_cast<int>(blockIdx.x) - merge_blocks;
   const int seg = id / per;
   const int b = seg / p.H_kv, hk = seg % p.H_kv;
@@ -1169,7 +1169,7 @@ __global__ void __launch_bounds__(FIN_THREADS)
   // The first rows' scores and the slots' weights are on their way while the LSEs form.
   const int t = t0 + warp;
   const bool on = t < n;
-  const float* x = xs + (static_cast<size_t>(seg) * tiles_max + t) * R * BN + 4 * lane;
+  const float* x = xs + (static_cast<size_t>(seg) * seqs.tiles + t - f) * R * BN + 4 * lane;
   float* dst = sh.key_weights + static_cast<size_t>(seg) * sh.slots + t * BN + 4 * lane;
   constexpr int AHEAD = 8;
   float4 v[AHEAD];
@@ -1219,8 +1219,8 @@ struct Workspace {
 };
 
 // Partials for (B H_kv + CTAs) slots, the segments' first and last group, and
-// with weights the shaped scores of every tile.
-Workspace carve(void* base, long long B, int H_kv, long long n_rows, int D, int max_len,
+// with weights the shaped scores of every tile that is walked.
+Workspace carve(void* base, long long B, int H_kv, long long n_rows, int D, int tiles,
                 bool weights) {
   auto r256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   Workspace w = {};
@@ -1238,7 +1238,7 @@ Workspace carve(void* base, long long B, int H_kv, long long n_rows, int D, int 
   w.t.seg_first = reinterpret_cast<int*>(take(segs * 4));
   w.t.seg_last = reinterpret_cast<int*>(take(segs * 4));
   if (weights)
-    w.xs = reinterpret_cast<float*>(take(segs * ((max_len + BN - 1) / BN) * BN * n_rows * 4));
+    w.xs = reinterpret_cast<float*>(take(segs * tiles * BN * n_rows * 4));
   return w;
 }
 
@@ -1257,8 +1257,15 @@ cudaError_t launch_nq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 
 Lens lens_of(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh) {
   const long long reach = sh.window > 0 ? static_cast<long long>(sh.window) + d.q_len - 1 : INT_MAX;
+  const long long most = (p.max_seqlen + BN - 1ll) / BN;
   return {d.cache_seqlens, p.B, p.max_seqlen,
-          static_cast<int>(min(reach, static_cast<long long>(INT_MAX)))};
+          static_cast<int>(min(reach, static_cast<long long>(INT_MAX))),
+          static_cast<int>(min(most, (reach + BN - 1) / BN + 1))};
+}
+
+Workspace workspace_of(const AttnParams& p, const DecodeArgs& d, const DecodeShapeArgs& sh,
+                       void* base) {
+  return carve(base, p.B, p.H_kv, d.n_rows, p.D, lens_of(p, d, sh).tiles, sh.key_weights != nullptr);
 }
 
 template <int D>
@@ -1284,13 +1291,10 @@ cudaError_t launch_finish(const AttnParams& p, const DecodeArgs& d, const Decode
                           const Workspace& w, cudaStream_t stream) {
   const Lens seqs = lens_of(p, d, sh);
   const long long rows = static_cast<long long>(p.B) * p.H_kv * d.n_rows;
-  const int tiles_max = (p.max_seqlen + BN - 1) / BN;
-  const int walked = static_cast<int>(
-      min(static_cast<long long>(tiles_max), (static_cast<long long>(seqs.reach) + BN - 1) / BN + 1));
   const long long merge = (rows + FIN_THREADS / 32 - 1) / (FIN_THREADS / 32);
   const long long blocks =
       merge + (sh.key_weights ? static_cast<long long>(p.B) * p.H_kv *
-                                   ((walked + FIN_TILES - 1) / FIN_TILES)
+                                   ((seqs.tiles + FIN_TILES - 1) / FIN_TILES)
                              : 0);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   // Launched while the ranges still run; it waits for them before it reads.
@@ -1304,7 +1308,7 @@ cudaError_t launch_finish(const AttnParams& p, const DecodeArgs& d, const Decode
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, finish_kernel<D>, p, d, w.t, sh, seqs,
-                            static_cast<const float*>(w.xs), static_cast<int>(merge), tiles_max, walked);
+                            static_cast<const float*>(w.xs), static_cast<int>(merge));
 }
 
 }  // namespace sdec
@@ -1312,13 +1316,13 @@ cudaError_t launch_finish(const AttnParams& p, const DecodeArgs& d, const Decode
 
 size_t decode_shaped_workspace(long long B, int H_kv, long long n_rows, int D, int max_len,
                                bool weights) {
-  return sdec::carve(nullptr, B, H_kv, n_rows, D, max_len, weights).bytes;
+  return sdec::carve(nullptr, B, H_kv, n_rows, D, static_cast<int>((max_len + sdec::BN - 1ll) / sdec::BN),
+                     weights).bytes;
 }
 
 cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,
                                  const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream) {
-  const sdec::Workspace w = sdec::carve(workspace, p.B, p.H_kv, d.n_rows, p.D, p.max_seqlen,
-                                        sh.key_weights != nullptr);
+  const sdec::Workspace w = sdec::workspace_of(p, d, sh, workspace);
   const cudaError_t e = p.D == 64 ? sdec::launch_walk<64>(p, d, sh, w, stream)
                                   : sdec::launch_walk<128>(p, d, sh, w, stream);
   return e == cudaSuccess ? launch_decode_finish(p, d, sh, workspace, stream) : e;
@@ -1326,8 +1330,7 @@ cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,
 
 cudaError_t launch_decode_finish(const AttnParams& p, const DecodeArgs& d,
                                  const DecodeShapeArgs& sh, void* workspace, cudaStream_t stream) {
-  const sdec::Workspace w = sdec::carve(workspace, p.B, p.H_kv, d.n_rows, p.D, p.max_seqlen,
-                                        sh.key_weights != nullptr);
+  const sdec::Workspace w = sdec::workspace_of(p, d, sh, workspace);
   return p.D == 64 ? sdec::launch_finish<64>(p, d, sh, w, stream)
                    : sdec::launch_finish<128>(p, d, sh, w, stream);
 }

@@ -142,7 +142,8 @@ cudaError_t launch_shaped_bwd(const AttnParams& p, const ShapeArgs& sh, void* ti
                               cudaStream_t stream);
 cudaError_t launch_key_ranges(const AttnParams& p, const int* doc_ids, const int* prefix_lens,
                               int window, int* key_begin, int* key_end, cudaStream_t stream);
-// n_rows = q_len H / H_kv <= 64, D = 64 or 128 (decode_shaped.cu).
+// n_rows = q_len H / H_kv <= 64, D = 64 or 128 (decode_shaped.cu). ``max_len``: under a
+// window no more than DecodeShapeArgs::window + q_len + 127.
 size_t decode_shaped_workspace(long long B, int H_kv, long long n_rows, int D, int max_len,
                                bool weights);
 cudaError_t launch_decode_shaped(const AttnParams& p, const DecodeArgs& d,

@@ -170,8 +170,11 @@ fa_status fa_decode_shaped(const void* q, const void* k_cache, const void* v_cac
   if (d.n_rows > 64) return FA_ERR_UNSUPPORTED;
   if ((shape->key_positions || shape->key_weights) && shape->slots < max_seqlen_k)
     return FA_ERR_INVALID_ARG;
-  const size_t need = fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, max_seqlen_k,
-                                                      shape->key_weights != nullptr);
+  // Under a window the tiles of its window + q_len - 1 slots, which may start inside one.
+  const long long span = shape->window > 0 ? shape->window + q_len + 127ll : max_seqlen_k;
+  const size_t need = fa_decode_shaped_workspace_size(
+      B, q_len, H, H_kv, D, static_cast<int>(std::min<long long>(max_seqlen_k, span)),
+      shape->key_weights != nullptr);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || !fa::aligned16(workspace)))
     return FA_ERR_INVALID_ARG;
   p.err.word = fa::err_word();

@@ -513,8 +513,8 @@ fa_status fa_key_ranges(const int* doc_ids, const int* prefix_lens, int window, 
  *   slots          row length of the two, >= max_seqlen_k
  * The rest as for fa_decode with n_split = 0, but at most 64 query rows share
  * a key/value head (q_len * H / H_kv <= 64, else FA_ERR_UNSUPPORTED). Results
- * are bitwise reproducible, whatever lies past a sequence's end. After FA_ERR_DEVICE_TIMEOUT key_weights, as the outputs,
- * may hold anything.
+ * are bitwise reproducible, whatever lies past a sequence's end. After
+ * FA_ERR_DEVICE_TIMEOUT key_weights, as the outputs, may hold anything.
  */
 typedef struct {
   float softcap;
@@ -526,7 +526,11 @@ typedef struct {
 } fa_decode_shape;
 
 /* fa_decode_shaped_workspace_size - bytes of workspace of fa_decode_shaped;
- * ``weights``: whether key_weights is set. Host only; 0 for invalid sizes. */
+ * ``weights``: whether key_weights is set. Host only; 0 for invalid sizes.
+ * About 4 q_len H (D + 1) bytes for each of B + 148 / H_kv partials, and with weights
+ * 4 q_len H bytes a slot of the B x max_seqlen_k (to a multiple of 128) for the scores.
+ * Under a window only the slots that a query may see have scores: pass
+ * min(max_seqlen_k, window + q_len + 127) for max_seqlen_k here, and that is enough. */
 size_t fa_decode_shaped_workspace_size(int B, int q_len, int H, int H_kv, int D, int max_seqlen_k,
                                        int weights);
 

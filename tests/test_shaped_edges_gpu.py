@@ -1,5 +1,7 @@
 """Edges of the shaped entry points on the GPU: workspaces in a bad state, values far from
 the usual, rows that belong to nobody, recipes of the documentation."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -176,3 +178,54 @@ def test_decode_bits_do_not_depend_on_pages_before_the_window(D):
                                 softcap=30.0, key_weights=w), w))
         clean()
     assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+# ------------------------------------------------------ workspace under a window ---
+
+@pytest.mark.parametrize("window,q_len", [(1, 1), (100, 1), (129, 8), (3000, 2), (1 << 30, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_window_needs_room_for_its_slots_only(D, window, q_len):
+    # The size that the header gives for a window, and not a byte behind it.
+    B, H, H_kv, most = 3, 8, 2, 4000
+    g = torch.Generator("cuda").manual_seed(window % 97)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    q, k, v = rnd(B * q_len, H, D), rnd(B * most, H_kv, D), rnd(B * most, H_kv, D)
+    lens = torch.tensor([most, 130, 2049], dtype=torch.int32, device="cuda")
+    lib, span = _abi.lib(), min(most, window + q_len + 127)
+    need = lib.fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, span, 1)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    w, w2 = (torch.zeros(B, H_kv, most, device="cuda") for _ in range(2))
+    o, lse = torch.empty_like(q), torch.empty(B * q_len, H, device="cuda")
+    shape = _abi.DecodeShape(30.0, None, window, None, w.data_ptr(), most)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), lens.data_ptr(), None,
+            B, q_len, H, H_kv, D, most, 0, B * most, most, 1, -1.0, ctypes.byref(shape), ws.data_ptr())
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.fa_decode_shaped(*args, need - 1, stream) == _abi.FA_ERR_INVALID_ARG
+    assert lib.fa_decode_shaped(*args, need, stream) == _abi.FA_OK
+    clean()
+    assert (ws[need:] == 0xA5).all()
+    big = torch.empty(lib.fa_decode_shaped_workspace_size(B, q_len, H, H_kv, D, most, 1),
+                      dtype=torch.uint8, device="cuda")
+    o2, lse2 = fa.decode(q, k, v, lens, q_len=q_len, max_seqlen_k=most, softcap=30.0, window=window,
+                         key_weights=w2, workspace=big)
+    clean()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(w, w2)
+    # every query's weights add up to one
+    assert torch.allclose(w.sum(-1), torch.tensor(float(q_len * H // H_kv), device="cuda"), rtol=1e-3)
+
+
+def test_decode_window_allocates_for_its_slots_only():
+    B, H, H_kv, D, most, window = 4, 16, 2, 64, 32768, 200
+    q = torch.randn(B * 8, H, D, device="cuda").bfloat16()
+    k, v = (torch.zeros(B * most, H_kv, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    lens = torch.full((B,), most, dtype=torch.int32, device="cuda")
+    w = torch.zeros(B, H_kv, most, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    out = fa.decode(q, k, v, lens, q_len=8, max_seqlen_k=most, softcap=30.0, window=window, key_weights=w)
+    clean()
+    used = torch.cuda.max_memory_allocated() - before
+    size = lambda n: _abi.lib().fa_decode_shaped_workspace_size(B, 8, H, H_kv, D, n, 1)
+    results = sum(x.numel() * x.element_size() for x in out)
+    assert used <= size(window + 8 + 127) + results + 4096 < size(most) // 4
