@@ -1,6 +1,8 @@
 """Edges of the shaped entry points on the GPU: workspaces in a bad state, values far from
 the usual, rows that belong to nobody, recipes of the documentation."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -229,3 +231,44 @@ def test_decode_window_allocates_for_its_slots_only():
     size = lambda n: _abi.lib().fa_decode_shaped_workspace_size(B, 8, H, H_kv, D, n, 1)
     results = sum(x.numel() * x.element_size() for x in out)
     assert used <= size(window + 8 + 127) + results + 4096 < size(most) // 4
+
+
+# -------------------------------------------------------------- the README ---
+
+def test_readme_of_shaped_scores_on_sequences_of_different_lengths():
+    # Its code as it stands, over two sequences of which one is shorter than what is kept.
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code, = [c for c in re.findall(r"```python\n(.*?)```", text, re.S) if "fa.evict(" in c]
+    B, H, H_kv, D, N, keep, recent, cap = 2, 4, 2, 64, 200, 2048, 64, 50.0
+    lengths, max_len = [2500, 700], 2600
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(s, generator=g).bfloat16() * 2
+    t = dict(q=rnd(B, N, H, D), k=rnd(B, N, H_kv, D), v=rnd(B, N, H_kv, D), dout=rnd(B, N, H, D),
+             slopes=torch.full((H,), 0.1), ids=torch.arange(B * N, dtype=torch.int32).view(B, N) // 70,
+             k_cache=rnd(B * max_len, H_kv, D), v_cache=rnd(B * max_len, H_kv, D), q_last=rnd(B, H, D),
+             lens=torch.tensor(lengths, dtype=torch.int32), q_new=rnd(B, H, D), k_new=rnd(B, H_kv, D),
+             v_new=rnd(B, H_kv, D))
+    names = {n: x.cuda() for n, x in t.items()}
+    names.update(torch=torch, B=B, H_kv=H_kv, max_len=max_len)
+    exec(code, names)
+    clean()
+    e = score_error(torch.cat([t["q_new"], t["q_last"]]), torch.cat([t["k_cache"], t["k_new"]]), D ** -0.5,
+                    cap, None, max_len, "bf16")
+    assert names["lens2"].tolist() == [keep + 1, 701]
+    pos, w = names["pos2"].cpu(), names["w"].cpu().numpy()
+    for b, n in enumerate(lengths):
+        m = int(names["lens2"][b])
+        for h in range(H_kv):
+            at = osh.kept_slots(w[b, h], n, keep, recent)
+            assert pos[b, h, :m].tolist() == at.tolist() + [n] and (pos[b, h, m:] == -1).all()
+            kk = torch.cat([t["k_cache"][b * max_len + at][:, h:h + 1], t["k_new"][b, h:h + 1][None]])
+            vv = torch.cat([t["v_cache"][b * max_len + at][:, h:h + 1], t["v_new"][b, h:h + 1][None]])
+            heads = slice(h * H // H_kv, (h + 1) * H // H_kv)
+            ro, rl, ra, rw = osh.decode(t["q_new"][b:b + 1, heads], kk, vv, [m], q_len=1, scale=D ** -0.5,
+                                        page_size=m, cap=cap, positions=pos[b:b + 1, h:h + 1, :m].numpy())
+            inside("O", f64(names["o"])[b:b + 1, heads], ro, (HALF + 2 * e) * ra + HALF * abs(ro))
+            inside("LSE", f64(names["lse"])[b:b + 1, heads], rl, e)
+            w0 = np.concatenate([w[b, h][at].astype(np.float64), [0.0]])
+            inside("weights", f64(names["w2"])[b, h, :m], w0 + rw[0, 0],
+                   2 * e * rw[0, 0] + 2.0 ** -22 * (1 + w0 + rw[0, 0]))
