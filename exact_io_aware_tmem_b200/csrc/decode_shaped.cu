@@ -1092,13 +1092,13 @@ __device__ __forceinline__ float pieces_lse(const DecodeTArgs& dt, const Pieces&
 // LSE) O_c. Segments inside one CTA's range were written by that CTA; empty sequences
 // get O = 0 and LSE = -inf here. The others: key_weights[b, hk, j] += sum_r 2^(z_rj -
 // LSE_r log2 e), FIN_TILES tiles of a segment per block, a warp a tile, four slots a lane.
+// (xs has no __restrict__: the first kernel still writes it when this one starts.)
 constexpr int FIN_THREADS = 128;
 constexpr int FIN_TILES = FIN_THREADS / 32;
 template <int D>
 __global__ void __launch_bounds__(FIN_THREADS)
     finish_kernel(const AttnParams p, const DecodeArgs dec, const DecodeTArgs dt,
-                  const DecodeShapeArgs sh, const Lens seqs, const float* __restrict__ xs,
-                  int merge_blocks) {
+                  const DecodeShapeArgs sh, const Lens seqs, const float* xs, int merge_blocks) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int R = dec.n_rows;
   if (static_cast<int>(blockIdx.x) < merge_blocks) {

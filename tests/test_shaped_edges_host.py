@@ -1,4 +1,8 @@
 """Edges of the shaped entry points without a GPU."""
+import glob
+import os
+import re
+
 import pytest
 
 from exact_io_aware_tmem_b200 import _abi
@@ -22,3 +26,17 @@ def test_selftest_decode_finish_arguments(lib, kw, code):
              slots=100, ws=256, ws_bytes=1 << 30)
     a.update(kw)
     assert lib.fa_selftest_decode_finish(*a.values(), None) == code
+
+
+def test_kernels_that_start_early_take_no_restrict_pointers():
+    # Such a kernel starts before the one ahead of it in the stream has ended: a pointer
+    # that promises memory nobody writes meanwhile would allow non-coherent loads of it.
+    csrc = os.path.join(os.path.dirname(_abi.__file__), "csrc")
+    early = []
+    for path in glob.glob(os.path.join(csrc, "*.cu")):
+        for kernel in open(path).read().split("__global__")[1:]:
+            body = kernel[:kernel.index("\n}\n")]
+            if "wait_for_primary();" in body:
+                early.append(re.search(r"(\w+_kernel)\(", body).group(1))
+                assert "__restrict__" not in body[:body.index(") {")], early[-1]
+    assert sorted(early) == ["finish_kernel", "move_kernel", "shaped_bwd_kernel"]
