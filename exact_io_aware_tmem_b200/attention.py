@@ -46,9 +46,16 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The handle alone, 0.05 us instead of 2.2 through a Stream object. Not a public name of
+# torch: where a release lacks it, the public one serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
     index = torch.cuda.current_device() if device.index is None else device.index
-    return torch._C._cuda_getCurrentRawStream(index)
+    if _raw_stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return _raw_stream(index)
 
 
 def _shape(q: torch.Tensor, k: torch.Tensor, cu_seqlens, max_seqlen):

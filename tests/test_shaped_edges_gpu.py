@@ -272,3 +272,16 @@ def test_readme_of_shaped_scores_on_sequences_of_different_lengths():
             w0 = np.concatenate([w[b, h][at].astype(np.float64), [0.0]])
             inside("weights", f64(names["w2"])[b, h, :m], w0 + rw[0, 0],
                    2 * e * rw[0, 0] + 2.0 ** -22 * (1 + w0 + rw[0, 0]))
+
+
+# ------------------------------------------------------------------ streams ---
+
+def test_stream_by_either_name(monkeypatch):
+    from exact_io_aware_tmem_b200 import attention
+    dev, side = torch.device("cuda", 0), torch.cuda.Stream()
+    for stream in (torch.cuda.default_stream(), side):
+        with torch.cuda.stream(stream):
+            ours = attention._stream(dev)
+            with monkeypatch.context() as m:
+                m.setattr(attention, "_raw_stream", None)
+                assert attention._stream(dev) == ours == stream.cuda_stream

@@ -4,8 +4,9 @@ import os
 import re
 
 import pytest
+import torch
 
-from exact_io_aware_tmem_b200 import _abi
+from exact_io_aware_tmem_b200 import _abi, attention
 
 
 @pytest.fixture(scope="module")
@@ -40,3 +41,12 @@ def test_kernels_that_start_early_take_no_restrict_pointers():
                 early.append(re.search(r"(\w+_kernel)\(", body).group(1))
                 assert "__restrict__" not in body[:body.index(") {")], early[-1]
     assert sorted(early) == ["finish_kernel", "move_kernel", "shaped_bwd_kernel"]
+
+
+def test_stream_without_the_private_name(monkeypatch):
+    class Stream:
+        cuda_stream = 4711
+    asked = []
+    monkeypatch.setattr(attention, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or Stream)
+    assert attention._stream(torch.device("cuda", 3)) == 4711 and asked == [3]
