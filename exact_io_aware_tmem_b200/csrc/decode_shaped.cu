@@ -514,7 +514,7 @@ __global__ void __launch_bounds__((Cfg<D, NQ>::THREADS), 1)
       // given back.
       if (lane < n_box && w.t * BN + lane * box < w.len &&
           w.t * BN + lane * box + box > first_slot(seqs, w.len)) {
-        if (blk >= 0 && static_cast<long long>(blk + 1) * dec.page <= dec.cache_rows)
+        if (blk >= 0 && (static_cast<long long>(blk) + 1) * dec.page <= dec.cache_rows)
           row = blk * dec.page + (box < BN ? 0 : (w.t - pg0 * tpp) * BN);
         else
           record_bounds(p.err, BAD_PAGE);

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           const int key = jt * BN + lane * box;
           int row = static_cast<int>(dec.cache_rows);
           if (key < len) {
-            if (blk >= 0 && static_cast<long long>(blk + 1) * dec.page <= dec.cache_rows)
+            if (blk >= 0 && (static_cast<long long>(blk) + 1) * dec.page <= dec.cache_rows)
               row = blk * dec.page + key % dec.page;
             else
               record_bounds(p.err, BAD_PAGE);

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int blk = __shfl_sync(FULL, kpb.cur, (pg0 + min(lane, n_box - 1) - kpb.base) & 31);
       int row = static_cast<int>(dec.cache_rows);
       if (lane < n_box && w.t * BN + lane * box < w.len) {
-        if (blk >= 0 && static_cast<long long>(blk + 1) * dec.page <= dec.cache_rows)
+        if (blk >= 0 && (static_cast<long long>(blk) + 1) * dec.page <= dec.cache_rows)
           row = blk * dec.page + (box < BN ? 0 : (w.t - pg0 * tpp) * BN);
         else
           record(p.err, BAD_PAGE);

@@ -160,6 +160,22 @@ def test_decode_bits_do_not_depend_on_rows_past_the_end(D, q_len, window, alibi,
         assert all(torch.equal(x, y) for x, y in zip(o, outs[0]))
 
 
+@pytest.mark.parametrize("page_id", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 25, 4, -1, -2 ** 31])
+@pytest.mark.parametrize("kw", [dict(softcap=30.0), dict(), dict(n_split=2)])
+def test_pages_outside_the_cache_are_reported(kw, page_id):
+    # Every id outside [0, 4), those whose first row leaves 32 bits among them; the shaped,
+    # the balanced and the split decode.
+    q = torch.randn(1, 4, 128, device="cuda").bfloat16()
+    k, v = (torch.randn(4 * 64, 2, 128, device="cuda").bfloat16() for _ in range(2))
+    lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+    for bad in range(4):
+        table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+        table[0, bad] = page_id
+        fa.decode(q, k, v, lens, q_len=1, max_seqlen_k=256, block_table=table, page_size=64, **kw)
+        assert fa.check_device_error()[0] == _abi.FA_ERR_INVALID_ARG
+    clean()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_decode_bits_do_not_depend_on_pages_before_the_window(D):
     # The pages that no query sees hold large keys, or have been given back.
