@@ -23,6 +23,9 @@ __device__ unsigned g_err_word[2];
 namespace {
 
 constexpr long long kDefaultBudget = 4000000000LL;  // ~2 s at 1.9 GHz
+// A kernel that gives up does not wait for its copies, which write its shared memory: by
+// this many cycles after the last of them was issued (10 ms) they have long landed.
+constexpr long long kLeastBudget = 20000000LL;
 
 // Last CUDA error behind an FA_ERR_CUDA on this host thread.
 thread_local cudaError_t g_last_cuda = cudaSuccess;
@@ -544,7 +547,7 @@ fa_status fa_check_device_error(fa_stream_t stream, unsigned* where) {
 }
 
 void fa_set_wait_budget(long long cycles) {
-  fa::g_budget = cycles > 0 ? cycles : fa::kDefaultBudget;
+  fa::g_budget = cycles > 0 ? std::max(cycles, fa::kLeastBudget) : fa::kDefaultBudget;
 }
 
 fa_status fa_selftest_wait_timeout(long long cycles, fa_stream_t stream) {

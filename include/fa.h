@@ -253,7 +253,9 @@ fa_status fa_check_device_error(fa_stream_t stream, unsigned* where);
 /*
  * fa_set_wait_budget - how many SM clock cycles one in-kernel wait may spin
  * before it gives up (default 4e9, about two seconds). Values <= 0 restore
- * the default. Applies to launches enqueued after the call.
+ * the default; values from 1 to 2e7 (about ten milliseconds) count as 2e7, so
+ * that a kernel that gives up leaves no copy of its own under way. Applies to
+ * launches enqueued after the call.
  */
 void fa_set_wait_budget(long long cycles);
 

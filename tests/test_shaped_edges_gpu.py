@@ -12,7 +12,8 @@ import exact_io_aware_tmem_b200 as fa
 from exact_io_aware_tmem_b200 import _abi
 from oracle import shaped as osh
 from tests._util import f64
-from tests.test_shaped_gpu import HALF, clean, inside, score_error
+from tests.test_shaped_gpu import (HALF, _agree, _all_of_it, _small_state, clean, inside,
+                                   score_error)
 
 pytestmark = pytest.mark.gpu
 
@@ -301,3 +302,17 @@ def test_stream_by_either_name(monkeypatch):
             with monkeypatch.context() as m:
                 m.setattr(attention, "_raw_stream", None)
                 assert attention._stream(dev) == ours == stream.cuda_stream
+
+
+def test_a_small_wait_budget_is_raised():
+    # No wait of these calls lasts ten milliseconds: all of them succeed.
+    s = _small_state(11)
+    _all_of_it(s)
+    clean()
+    fa.set_wait_budget(1)
+    try:
+        got = _all_of_it(s)
+        clean()
+    finally:
+        fa.set_wait_budget(0)
+    _agree(got, _all_of_it(s))
