@@ -10,6 +10,7 @@ import torch
 
 import exact_io_aware_tmem_b200 as fa
 from exact_io_aware_tmem_b200 import _abi
+from exact_io_aware_tmem_b200.workloads import decode_case, random_case
 from oracle import shaped as osh
 from tests._util import f64
 from tests.test_shaped_gpu import (HALF, _agree, _all_of_it, _small_state, clean, inside,
@@ -316,3 +317,92 @@ def test_a_small_wait_budget_is_raised():
     finally:
         fa.set_wait_budget(0)
     _agree(got, _all_of_it(s))
+
+
+# ------------------------------------------------------------- negative slopes ---
+
+@pytest.mark.parametrize("steep", [-0.01, -0.2, -2.0])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 40)])
+def test_negative_slopes(dtype, D, causal, cap, steep):
+    # They favour the far keys: the softmax's reference moves at every tile. One head's slope
+    # is positive beside them.
+    lengths, H, H_kv = [333, 333], 4, 2
+    N, T = 333, 666
+    inp = random_case(17, dtype=dtype, lengths=lengths, H=H, H_kv=H_kv, D=D, varlen=False)
+    slopes = torch.tensor([steep, 0.5 * steep, -0.3 * steep, 0.1 * steep])
+    dev = lambda t: t.cuda().view(2, N, *t.shape[1:]).contiguous()
+    kw = dict(causal=causal, softcap=cap or None, alibi_slopes=slopes.cuda())
+    q, k, v, do = dev(inp.q), dev(inp.k), dev(inp.v), dev(inp.do)
+    o, lse = fa.fwd(q, k, v, **kw)
+    got = fa.bwd(do, q, k, v, o, lse, **kw)
+    clean()
+    args = (inp.cu_seqlens.tolist(), causal, D ** -0.5, cap, slopes)
+    r = osh.forward(inp.q, inp.k, inp.v, *args)
+    b = osh.backward(inp.q, inp.k, inp.v, inp.do, *args)
+    # The bounds of the other cases; the scores reach |slope| N.
+    e = score_error(inp.q, inp.k, D ** -0.5, cap, slopes.abs(), N, dtype)
+    h = HALF if dtype == "bf16" else 2.0 ** -23
+    inside("LSE", f64(lse).transpose(1, 0, 2).reshape(H, T), r.lse, e)
+    inside("O", f64(o).reshape(T, H, D), r.o,
+           (h * (1 + 2 * h) + 2 * e) * (r.o_abs + abs(r.o)) + h * abs(r.o))
+    dq, dk, dv = (f64(x).reshape(y.shape) for x, y in zip(got, (b.dq, b.dk, b.dv)))
+    tiny = e + D * 2.0 ** -23
+    c = 2.0 ** -20 if cap else 0.0
+    f = 2.0 ** -39 if dtype == "bf16" else 0.0
+    inside("dV", dv, b.dv, (h + 2 * e) * b.dv_abs + h * abs(b.dv))
+    for name, x, y, one, raw, full, delta in (("dQ", dq, b.dq, b.dq_one, b.dq_raw, b.dq_abs, b.dq_del),
+                                              ("dK", dk, b.dk, b.dk_one, b.dk_raw, b.dk_abs, b.dk_del)):
+        inside(name, x, y, f * one + c * raw + (2 * h + 4 * e) * full + (h + 2 * tiny) * delta + h * abs(y))
+
+
+@pytest.mark.parametrize("page", [None, 64])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_negative_slopes_in_decode(D, cap, page):
+    lengths, q_len, H, H_kv, most = [1, 129, 700, 2000], 3, 8, 2, 2000
+    c = decode_case(21, dtype="bf16", lengths=lengths, q_len=q_len, H=H, H_kv=H_kv, D=D, page_size=page)
+    if page is None:
+        c.page_size = c.k_cache.shape[0] // len(lengths)
+    slopes = torch.linspace(-0.4, 0.2, H)
+    w = torch.zeros(len(lengths), H_kv, most, device="cuda")
+    o, lse = fa.decode(c.q.cuda(), c.k_cache.cuda(), c.v_cache.cuda(), c.cache_seqlens.cuda(), q_len=q_len,
+                       max_seqlen_k=most, page_size=c.page_size, softcap=cap or None,
+                       block_table=None if page is None else c.block_table.cuda(),
+                       alibi_slopes=slopes.cuda(), key_weights=w)
+    clean()
+    ro, rl, ra, rw = osh.decode(c.q, c.k_cache, c.v_cache, lengths, q_len=q_len, scale=D ** -0.5,
+                                page_size=c.page_size, block_table=c.block_table, cap=cap, slopes=slopes,
+                                slots=most)
+    used = torch.isfinite(c.k_cache[:, 0, 0].float())
+    e = score_error(c.q, c.k_cache[used], D ** -0.5, cap, slopes.abs(), most, "bf16")
+    inside("LSE", f64(lse), rl, e)
+    inside("O", f64(o), ro, (HALF + 2 * e) * ra + HALF * abs(ro))
+    inside("weights", f64(w), rw, 2 * e * rw + 2.0 ** -22 * (1 + rw))
+
+
+# ----------------------------------------------------------------- far offsets ---
+
+def test_gradients_of_keys_past_2_31_elements():
+    # 270 thousand tokens of 64 heads of 128, each seeing its last 40 keys: dK and dV of the
+    # last tokens, whose queries all lie among the last ones too. Q and dO differ, so that a
+    # row taken from elsewhere shows.
+    N, H, D, window, m = 270_000, 64, 128, 40, 300
+    g = torch.Generator("cuda").manual_seed(3)
+    rnd = lambda h: torch.randn((1, N, h, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    q, do, k, v = rnd(H), rnd(H), rnd(1), rnd(1)
+    begin = (torch.arange(N, device="cuda") - window + 1).clamp(min=0).int()[None]
+    kw = dict(causal=True, softcap=30.0, key_begin=begin)
+    o, lse = fa.fwd(q, k, v, **kw)
+    _, dk, dv = fa.bwd(do, q, k, v, o, lse, **kw)
+    clean()
+    qq, gg, kk, vv = (x[0, N - m:].cpu() for x in (q, do, k, v))
+    b = osh.backward(qq, kk, vv, gg, [0, m], True, D ** -0.5, 30.0, None,
+                     np.maximum(0, np.arange(m) - window + 1))
+    e = score_error(qq, kk, D ** -0.5, 30.0, None, m, "bf16")
+    s = slice(window, m)   # from here on the queries see only keys among the last m
+    inside("dV", f64(dv[0, N - m:])[s], b.dv[s], ((HALF + 2 * e) * b.dv_abs + HALF * abs(b.dv))[s])
+    inside("dK", f64(dk[0, N - m:])[s], b.dk[s],
+           (2.0 ** -39 * b.dk_one + 2.0 ** -20 * b.dk_raw + (2 * HALF + 4 * e) * b.dk_abs +
+            (HALF + 2 * (e + D * 2.0 ** -23)) * b.dk_del + HALF * abs(b.dk))[s])
