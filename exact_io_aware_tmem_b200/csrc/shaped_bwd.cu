@@ -28,9 +28,12 @@
 // - The cap per 32 scores by the shortest polynomial that their largest allows, or by
 //   exponential and reciprocal (score_cap.cuh).
 //
-// B1 H16/4 N8192 D128 causal, cap 50: 980 us of a 1530 us step, 700 TFLOP/s (the unshaped
-// fused backward takes 859 with its D); bound by the chain of the warps that form P and
-// dX, which the cap and 1 - t^2 lengthen, as the unshaped one is by its own.
+// B1 H16/4 N8192 D128 causal, cap 50: 980 us of a step of 1541 us after a rest (1665 back
+// to back, under the power cap), 700 TFLOP/s (the unshaped fused backward takes 859 with
+// its D); bound by the chain of the warps that form P and dX, which the cap and 1 - t^2
+// lengthen, as the unshaped one is by its own. At D = 128 the forms with a cap spill: 24
+// bytes of stores and 144 of loads a thread without a bias, 8 and 28 with one; the others
+// nothing.
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>

@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     if (threadIdx.x == 0) record_bounds(p.err, BAD_ALIGN);
     return;
   }
-  // Rows of no sequence, if the tensors have any, get a dQ of zero.
+  // Rows behind the last sequence, which total_tokens == cu_seqlens[B] rules out, get a dQ
+  // of zero all the same, as from the unshaped backward: the conversion reads every row.
   if (blockIdx.x == 0 && p.cu_seqlens != nullptr) {
     const long long end = max(0, __ldg(p.cu_seqlens + p.B)), row = static_cast<long long>(p.H) * D;
     for (long long i = end * row + threadIdx.x; i < p.total * row; i += C::THREADS) p.dq_accum[i] = 0.f;

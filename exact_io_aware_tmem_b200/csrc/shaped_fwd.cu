@@ -22,17 +22,21 @@
 // the cap costs five products on packed pairs a score pair and the exponential one of 16
 // lanes a clock, and four warps a scheduler keep both busy.
 //
-// What bounds it: that arithmetic, and a start and end of about 10 us a CTA that
-// nothing overlaps at D = 128. B2 H16 N8192 D128 causal, cap 50: 540 us (1018 TFLOP/s;
-// the products alone would be 335 us, the unshaped forward is 466). B4 H16 N2048 D64
-// causal, bias: 82 us, where one exponential a score is 30 us.
+// What bounds it: the latency of a softmax warp's chain from scores to P (no unit is full:
+// tensor core and special-function unit 48 % each, issue 45 %), and a start and end of
+// about 10 us a CTA that nothing overlaps at D = 128. B2 H16 N8192 D128 causal, cap 50: 566
+// us a call after a rest (971 TFLOP/s), 627 back to back under the power cap; the products
+// alone would be 335 us, the unshaped forward is 466. B4 H16 N2048 D64 causal, bias: 82 us,
+// where one exponential a score is 30 us. Every form with a running maximum spills 12 to 64
+// bytes a thread at its 96 registers.
 //
 // One reading of S. The reference a tile's P are taken at is the maximum of the tiles
 // before it (the halves' maxima meet in shared memory; the next step's S orders
 // that); the tile's own maximum is found beside its exponentials. Only if a score
 // exceeds the reference by 2^64, or a row's first visible tile lies below 2^-20 of
 // reference 0, is the tile read again for its maximum first; the two warps of the
-// same rows agree on that with one barrier.
+// same rows agree on that with one barrier. A bias can make that the rule where its
+// favourites come last: see the order of the tiles below.
 //
 // The cap. Up to |s| <= 0.4 cap / scale a polynomial of four terms, up to 0.8 cap /
 // scale one of six (score_cap.cuh), which leave the special-function unit to the one
@@ -389,7 +393,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   // takes part in the steps [b_g, f_g). With a bias from the end: under a causal mask
   // the keys nearest to the queries, which the bias favours, then come first and set
   // the reference for good (91 against 127 us on B4 H16 N2048 D64); without one the
-  // order makes no difference (571 us on B2 H16 N8192 D128 with a cap either way).
+  // order makes no difference (571 us on B2 H16 N8192 D128 with a cap either way). Where
+  // queries see keys behind them too, an early one starts with its farthest: each tile on
+  // its way to the diagonal moves the reference, or is read again where the bias grows by
+  // 2^64 within it (the same case not causal, slopes of 2^(-h/2): 257 us; of 0.6: 294; the
+  // unshaped forward 120; negative slopes, causal, -0.6: 217).
   const bool any_0 = s_hi[0] > 0, any_1 = G > 1 && s_hi[1] > 0;
   const int t_0 = any_0 ? s_lo[0] / BN : INT_MAX, t_1 = any_1 ? s_lo[1] / BN : INT_MAX;
   const int e_0 = (s_hi[0] + BN - 1) / BN, e_1 = any_1 ? (s_hi[1] + BN - 1) / BN : 0;
